@@ -1,0 +1,181 @@
+/*
+ * fusedmx.h — C ABI of the B200 (sm_100a) operators that consume MXFP4 rows,
+ * libfusedmx.so: the product of two MXFP4 operands on the block-scaled tensor
+ * cores, the same product with one weight per expert over ragged row ranges,
+ * the gated activation with the quantization of its result, and the weighted
+ * sum of expert rows.  They take and give the tuples of fusednorm.h:
+ *
+ *   fn_rmsnorm_quant -> mx_grouped_gemm -> mx_silu_mul_quant -> mx_grouped_gemm
+ *     -> mx_combine (-> a partial of the next fn_rmsnorm_quant)
+ *
+ * Conventions for every entry point (those of fusednorm.h, whose status codes,
+ * modes and layout flags are used here too):
+ *  - Every data pointer is a DEVICE pointer owned by the caller, memory of the
+ *    current device.  The library allocates nothing and never synchronizes: work
+ *    is queued on `stream` (a cudaStream_t passed as void*; NULL means the legacy
+ *    default stream).  No workspace: calls on any number of streams, threads and
+ *    captured graphs are independent of each other.
+ *  - All argument checks run on the host before anything is launched; on any error
+ *    nothing is launched and no output is touched.  A call without rows returns
+ *    FN_OK and launches nothing once the sizes and flags are valid; the data
+ *    pointers are not examined then and may be NULL.
+ *  - Row indices and counts that live on the device cannot be checked on the host:
+ *    the kernels keep every access inside the buffers whatever they hold.
+ *  - A launch that the CUDA runtime rejects returns FN_ERR_CUDA.
+ *  - Every sum has a fixed order: the same call on the same inputs gives the same
+ *    bits.
+ *  - Every device-side wait is bounded; should one ever run out (not seen on
+ *    working hardware), the outputs that are still due are written as NaN.
+ */
+#ifndef FUSEDMX_H
+#define FUSEDMX_H
+
+#include <stdint.h>
+
+#include "fusednorm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Output type of the products, OR-ed into `flags` (one of the three). */
+#define MX_OUT_BF16 0x0
+#define MX_OUT_FP16 0x1
+#define MX_OUT_FP32 0x2
+/* Scale layouts of the operands, OR-ed into `flags`: without the flag E8M0
+ * bytes row-major [rows, K/32], with it the 32x4x4 tiling that
+ * FN_SCALE_SWIZZLE_32_4_4 describes (16-byte aligned). */
+#define MX_A_SCALE_SWIZZLE 0x10
+#define MX_B_SCALE_SWIZZLE 0x20
+
+#define MX_MAX_EXPERTS 1024
+#define MX_MAX_TOP 32
+
+/*
+ * Product of two MXFP4 operands (a linear layer on quantized rows):
+ *     out[m, n] = round( sum_g 2^(sa[m,g] + sb[n,g] - 254)
+ *                              sum_{k in group g} a[m, k] * b[n, k] )
+ * with groups of 32 elements, sums in fp32 on the tensor cores and one rounding
+ * to the output type (nearest even; fp32 output: none).  A scale byte of 0xFF
+ * is NaN and makes the sums it takes part in NaN.
+ *
+ * a_q      E2M1 codes of M rows, u8 [M, K/2] (element 2i in the low nibble of
+ *          byte i), as fn_quant and fn_rmsnorm_quant write them.
+ * a_scale  E8M0 bytes of the rows, [M, K/32] or swizzled.
+ * b_q      codes of the weight, u8 [N, K/2] (row n holds output n's weights).
+ * b_scale  E8M0 bytes of the weight, [N, K/32] or swizzled.
+ * M        >= 0.  N >= 1.  K a multiple of 32, >= 32.  (M and N at most
+ *          2^31 - 257, K at most 2^24; more is FN_ERR_UNSUPPORTED.)
+ * out      [M, N] of the output type, rows ldo elements apart (ldo >= N, at most
+ *          2^28; more is FN_ERR_UNSUPPORTED).
+ *          Elements between N and ldo are not written.
+ * Alignment  a_q and b_q 16 bytes; swizzled scales 16 bytes; out its element
+ *          size.  Otherwise FN_ERR_ALIGN.  Padding of swizzled scales is not
+ *          used whatever it holds.
+ * Overlap  out must not overlap an input (FN_ERR_INVALID).
+ */
+FN_API int mx_gemm(const void* a_q, const void* a_scale, const void* b_q, const void* b_scale,
+                   int64_t M, int64_t N, int64_t K, int flags, void* out, int64_t ldo,
+                   void* stream);
+
+/*
+ * The product with one weight for each of E experts over ragged row ranges:
+ * expert e owns the rows offsets[e] <= r < offsets[e + 1], and
+ *     out[r, n] = round( sum over k of A[src(r), k] * B[e][n, k] ),
+ * src(r) = rows[r] if `rows` is given, else r.  An expert may own no row.
+ * Rows of out that no expert owns are left as they were (rows in front of
+ * offsets[0] and from offsets[E] on).
+ *
+ * a_q, a_scale   as mx_gemm, a_rows rows; scales row-major only
+ *          (MX_A_SCALE_SWIZZLE is FN_ERR_UNSUPPORTED: a row range starts
+ *          anywhere in the tiling).
+ * rows     int32 [R] or NULL (then a_rows >= R).  A row whose index is outside
+ *          [0, a_rows) gives a row of zeros.  An index may occur any number
+ *          of times.
+ * offsets  int32 [E + 1], non-decreasing, in [0, R].  Values outside are
+ *          clamped into [0, R], and a range that runs backwards is empty;
+ *          where ranges overlap, the rows hold one of the owners' results.
+ * b_q      u8 [E, N, K/2];  b_scale [E, N, K/32], or swizzled: E tilings of
+ *          roundup(N,128) * roundup(K/32,4) bytes, one after another.
+ * R        rows of out, >= 0.  E: 1..MX_MAX_EXPERTS (above: FN_ERR_UNSUPPORTED).
+ * Other arguments, alignment (offsets and rows 4 bytes), overlap and limits
+ * as mx_gemm.
+ */
+FN_API int mx_grouped_gemm(const void* a_q, const void* a_scale, int64_t a_rows,
+                           const int32_t* rows, const int32_t* offsets, int64_t E,
+                           const void* b_q, const void* b_scale, int64_t R, int64_t N, int64_t K,
+                           int flags, void* out, int64_t ldo, void* stream);
+
+/*
+ * Gated activation and quantization of its result, one pass over the rows:
+ *     y[m, h] = round16( g * u / (1 + exp(-g)) ),  g = x[m, h], u = x[m, H + h]
+ *     (out_q, out_scale) = quantize(y, mode)
+ * y is the correctly rounded 16-bit value of the real number on the right (one
+ * rounding to nearest even), so codes and scales are those of fn_quant on that
+ * row, bit for bit.  NaN, and g = -infinity, give NaN.
+ *
+ * x        bf16 (or binary16 with FN_IO_FP16) [M, 2H]: the gate half, then the
+ *          up half; rows ldx elements apart (ldx >= 2H, a multiple of 8).
+ * mode     as fn_quant: fn_mode, optionally one FN_SCALE_* layout flag and
+ *          FN_IO_FP16.
+ * num_rows int32 [1] on the device, or NULL: only the rows below
+ *          min(M, max(0, *num_rows)) are read and written (a batch whose size
+ *          only the device knows); the others are left as they were.
+ * out_q, out_scale   as fn_quant.   out_y: 16-bit [M, H] or NULL.
+ * M, H, alignment and overlap as fn_quant (x: 16 bytes; num_rows: 4 bytes).
+ */
+FN_API int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H,
+                             const int32_t* num_rows, void* out_q, void* out_scale, void* out_y,
+                             void* stream);
+
+/*
+ * Weighted sum of expert rows back in token order:
+ *     out[t, :] = round16( base[t, :] + sum_j weight[t, j] * y[pos[t, j], :] )
+ * in fp32, j ascending, the base first.  A position outside [0, R) is skipped
+ * (a dropped choice): its row and its weight are not used.  A position may
+ * occur any number of times.
+ *
+ * y        bf16 (or binary16 with FN_IO_FP16 in `flags`) [R, N].
+ * pos      int32 [T, k].   weight: fp32 [T, k].   k: 0..MX_MAX_TOP.
+ * base     16-bit [T, N] or NULL (zero).   May be `out` itself (in place).
+ * out      16-bit [T, N].
+ * T, R     >= 0.   N >= 1, at most 2^24.   flags: 0 or FN_IO_FP16.
+ * Alignment  y, base and out 2 bytes (16-byte pointers and N % 8 == 0 take the
+ *          wide path); pos and weight 4 bytes.
+ * Overlap  out must not overlap another input than base (FN_ERR_INVALID).
+ */
+FN_API int mx_combine(const void* y, int64_t R, const int32_t* pos, const float* weight,
+                      const void* base, int64_t T, int k, int64_t N, int flags, void* out,
+                      void* stream);
+
+/* Which kernel the calling thread's last successful call launched (MX_VARIANT_NONE
+ * after an error or a call without rows). */
+typedef enum {
+    MX_VARIANT_NONE = 0,
+    MX_VARIANT_GEMM = 1,          /* mx_gemm, mx_grouped_gemm: one block per tile        */
+    MX_VARIANT_SILU_GROUPS = 2,   /* mx_silu_mul_quant, group modes                     */
+    MX_VARIANT_SILU_ROW = 3,      /* mx_silu_mul_quant, per-token mode                   */
+    MX_VARIANT_COMBINE = 4,       /* mx_combine, 16-byte vectors                         */
+    MX_VARIANT_COMBINE_NARROW = 5 /* mx_combine, single elements                         */
+} mx_variant;
+FN_API int mx_last_variant(void);
+
+/* Launch shape of the calling thread's last launch: out[0] blocks, out[1]
+ * threads per block; for the products out[2] token rows of a tile and out[3]
+ * blocks of a cluster (1: none). */
+FN_API void mx_last_launch(int32_t out[4]);
+
+/* As fn_programmatic_launch, for this library's calls of the calling thread. */
+FN_API int mx_programmatic_launch(int on);
+
+/* Static, NUL-terminated description of a status code. */
+FN_API const char* mx_status_string(int status);
+
+/* Library ABI version (major * 100 + minor). */
+FN_API int mx_version(void);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FUSEDMX_H */

@@ -1,7 +1,7 @@
-"""Build libfusednorm.so in-tree with nvcc for sm_100a.
+"""Build libfusednorm.so and libfusedmx.so in-tree with nvcc for sm_100a.
 
-The library is the product: the binding loads it from this directory and
-refuses to run without it.  IEEE division and square root, no flush-to-zero
+The libraries are the product: the bindings load them from this directory and
+refuse to run without them.  IEEE division and square root, no flush-to-zero
 and no fast-math, because the quantized codes are specified bit-exactly.
 The twelve (mode, partial-bound) kernel units compile in parallel.
 """
@@ -32,10 +32,15 @@ UNITS = [("fusednorm", "fusednorm.cu", [])] + [
 ] + [(f"ar_{mode}", "ar_inst.cu", [f"-DFN_INST_MODE={mode}"]) for mode in (0, 1, 2)] + [
     ("hc", "hc_inst.cu", [])]
 
+# libfusedmx.so: the MXFP4 products and the operators between them
+LIB_MX = os.path.join(PKG, "libfusedmx.so")
+UNITS_MX = [("fusedmx", "fusedmx.cu", []), ("mg", "mg_inst.cu", [])]
+
 
 def deps():
     return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))] + \
-        [os.path.join(INCLUDE, "fusednorm.h"), os.path.abspath(__file__)]
+        [os.path.join(INCLUDE, f) for f in ("fusednorm.h", "fusedmx.h")] + \
+        [os.path.abspath(__file__)]
 
 
 def nvcc() -> str:
@@ -43,10 +48,10 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def up_to_date(lib=LIB) -> bool:
+    if not os.path.exists(lib):
         return False
-    t = os.path.getmtime(LIB)
+    t = os.path.getmtime(lib)
     return all(os.path.getmtime(d) <= t for d in deps())
 
 
@@ -61,26 +66,34 @@ def _compile(unit, extra, verbose):
     return obj, r
 
 
-def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and up_to_date() and not extra:
-        return LIB
+def _build(lib, units, force, verbose, extra) -> str:
+    if not force and up_to_date(lib) and not extra:
+        return lib
     os.makedirs(BUILD, exist_ok=True)
-    jobs = max(1, min(len(UNITS), os.cpu_count() or 1))
+    jobs = max(1, min(len(units), os.cpu_count() or 1))
     with ThreadPoolExecutor(jobs) as ex:
-        results = list(ex.map(lambda u: _compile(u, extra, verbose), UNITS))
+        results = list(ex.map(lambda u: _compile(u, extra, verbose), units))
     for obj, r in results:
         if r.returncode != 0 or (verbose and r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {obj}")
-    tmp = LIB + ".tmp"
+    tmp = lib + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "--cudart", "static", "-o", tmp, *[o for o, _ in results]]
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
+    return _build(LIB, UNITS, force, verbose, extra)
+
+
+def build_mx_library(force: bool = False, verbose: bool = False, extra=()) -> str:
+    return _build(LIB_MX, UNITS_MX, force, verbose, extra)
 
 
 if __name__ == "__main__":
-    build_library(force="--force" in sys.argv, verbose="--verbose" in sys.argv,
-                  extra=("-Xptxas", "-v") if "--ptxas-v" in sys.argv else ())
-    print(LIB)
+    for build in (build_library, build_mx_library):
+        print(build(force="--force" in sys.argv, verbose="--verbose" in sys.argv,
+                    extra=("-Xptxas", "-v") if "--ptxas-v" in sys.argv else ()))

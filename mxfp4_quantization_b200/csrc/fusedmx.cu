@@ -1,0 +1,439 @@
+// Host side of libfusedmx.so: argument checks, dispatch, launches.
+// The C ABI and its contract are declared in include/fusedmx.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "fusedmx.h"
+#include "act_kernel.cuh"
+#include "combine_kernel.cuh"
+#include "mg_params.h"
+
+namespace {
+
+thread_local int tl_variant = MX_VARIANT_NONE;
+thread_local int32_t tl_launch[4] = {0, 0, 0, 0};
+thread_local int tl_pdl = 0;
+
+struct Range {
+  uintptr_t lo, hi;  // [lo, hi)
+};
+
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+Range range_of(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Range{lo, lo + static_cast<uintptr_t>(bytes)};
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return -1;
+  }
+  return n;
+}
+
+template <typename... KArgs, typename... Args>
+int launch(void (*k)(KArgs...), unsigned grid, unsigned threads, size_t smem, void* stream,
+           int cluster, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (tl_pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = (unsigned)n;
+  if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FN_ERR_CUDA;
+  }
+  return FN_OK;
+}
+
+void record(int variant, int64_t a, int64_t b, int64_t c, int64_t d) {
+  tl_variant = variant;
+  tl_launch[0] = (int32_t)a;
+  tl_launch[1] = (int32_t)b;
+  tl_launch[2] = (int32_t)c;
+  tl_launch[3] = (int32_t)d;
+}
+
+// ---- the products -----------------------------------------------------------------------
+
+// The driver's encoder of TMA descriptors, looked up once (the library does not
+// link against libcuda).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static std::atomic<EncodeTiled> cached{nullptr};
+  EncodeTiled f = cached.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult res;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                       &res) != cudaSuccess ||
+      res != cudaDriverEntryPointSuccess || !p) {
+    (void)cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeTiled>(p);
+  cached.store(f, std::memory_order_release);
+  return f;
+}
+
+// Code rows [rows, K/2] bytes; boxes of 128 bytes x `box` rows, swizzled.
+bool code_map(CUtensorMap* m, const void* q, int64_t rows, int64_t K, int box) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box};
+  const cuuint32_t elem[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, boxes, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory of a kernel, allowed once per kernel and device (function
+// attributes belong to a device's context).
+bool allow_smem(const void* k, int bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> done;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  int& have = done[std::make_pair(k, dev)];
+  if (have >= bytes) return true;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  have = bytes;
+  return true;
+}
+
+struct Product {
+  const void *a_q, *a_scale, *b_q, *b_scale;
+  const int32_t *rows, *offsets;
+  int64_t a_rows, E, M, N, K, ldo;
+  int flags;
+  void* out;
+};
+
+constexpr int64_t kMaxRows = INT32_MAX - 256;  // row coordinates with a tile's reach on top
+constexpr int64_t kMaxK = 1 << 24;
+
+int64_t scale_bytes(int64_t rows, int64_t K, bool swizzled) {
+  return swizzled ? round_up(rows, 128) * round_up(K / 32, 4) : rows * (K / 32);
+}
+
+int out_size(int flags) { return (flags & 0xF) == MX_OUT_FP32 ? 4 : 2; }
+
+int check_product(const Product& q, bool grouped) {
+  const int known = 0xF | MX_A_SCALE_SWIZZLE | MX_B_SCALE_SWIZZLE;
+  if ((q.flags & ~known) || (q.flags & 0xF) > MX_OUT_FP32) return FN_ERR_INVALID;
+  if (q.M < 0 || q.N < 1 || q.K < 32 || q.K % 32 || q.ldo < q.N) return FN_ERR_INVALID;
+  if (grouped && (q.E < 1 || q.a_rows < 0)) return FN_ERR_INVALID;
+  if (q.M > kMaxRows || q.N > kMaxRows || q.K > kMaxK) return FN_ERR_UNSUPPORTED;
+  if (grouped) {
+    if (q.flags & MX_A_SCALE_SWIZZLE) return FN_ERR_UNSUPPORTED;
+    if (q.E > MX_MAX_EXPERTS || q.a_rows > kMaxRows || q.E * q.N > kMaxRows)
+      return FN_ERR_UNSUPPORTED;
+  }
+  // every address stays below 2^62 bytes from its pointer
+  if (q.ldo > ((int64_t)1 << 28)) return FN_ERR_UNSUPPORTED;
+  return FN_OK;
+}
+
+int check_product_pointers(const Product& q, bool grouped) {
+  if (!q.a_q || !q.a_scale || !q.b_q || !q.b_scale || !q.out) return FN_ERR_INVALID;
+  if (grouped && !q.offsets) return FN_ERR_INVALID;
+  if (grouped && (q.rows ? q.a_rows < 1 : q.a_rows < q.M)) return FN_ERR_INVALID;
+  if (!aligned(q.a_q, 16) || !aligned(q.b_q, 16) || !aligned(q.out, out_size(q.flags)))
+    return FN_ERR_ALIGN;
+  if ((q.flags & MX_A_SCALE_SWIZZLE && !aligned(q.a_scale, 16)) ||
+      (q.flags & MX_B_SCALE_SWIZZLE && !aligned(q.b_scale, 16)))
+    return FN_ERR_ALIGN;
+  if (grouped && (!aligned(q.offsets, 4) || !aligned(q.rows, 4))) return FN_ERR_ALIGN;
+  const Range out = range_of(q.out, ((q.M - 1) * q.ldo + q.N) * out_size(q.flags));
+  const int64_t E = grouped ? q.E : 1;
+  const int64_t b_scale = E * scale_bytes(q.N, q.K, q.flags & MX_B_SCALE_SWIZZLE);
+  if (overlap(out, range_of(q.a_q, q.a_rows * q.K / 2)) ||
+      overlap(out, range_of(q.a_scale,
+                            scale_bytes(q.a_rows, q.K, q.flags & MX_A_SCALE_SWIZZLE))) ||
+      overlap(out, range_of(q.b_q, E * q.N * q.K / 2)) ||
+      overlap(out, range_of(q.b_scale, b_scale)))
+    return FN_ERR_INVALID;
+  if (grouped && (overlap(out, range_of(q.offsets, (q.E + 1) * 4)) ||
+                  (q.rows && overlap(out, range_of(q.rows, q.M * 4)))))
+    return FN_ERR_INVALID;
+  return FN_OK;
+}
+
+int launch_product(const Product& q, bool grouped, void* stream) {
+  fn::MGParams p;
+  std::memset(&p, 0, sizeof p);
+  p.x_scale = static_cast<const uint8_t*>(q.a_scale);
+  p.w_scale = static_cast<const uint8_t*>(q.b_scale);
+  p.out = q.out;
+  p.offsets = q.offsets;
+  p.rows = q.rows;
+  p.ldo = q.ldo;
+  p.w_scale_stride = scale_bytes(q.N, q.K, q.flags & MX_B_SCALE_SWIZZLE);
+  p.M = (int)q.M;
+  p.x_rows = (int)q.a_rows;
+  p.N = (int)q.N;
+  p.K = (int)q.K;
+  p.E = grouped ? (int)q.E : 1;
+  p.groups = (int)(q.K / 32);
+  p.x_swizzled = q.flags & MX_A_SCALE_SWIZZLE ? 1 : 0;
+  p.w_swizzled = q.flags & MX_B_SCALE_SWIZZLE ? 1 : 0;
+  p.out_type = q.flags & 0xF;
+  const int sms = sm_count();
+  if (sms <= 0) return FN_ERR_CUDA;
+  const int64_t each = grouped ? (q.M + q.E - 1) / q.E : q.M;
+  const fn::MGInstance k = fn::mg_pick(each <= 16 ? 16 : each <= 64 ? 64 : each <= 128 ? 128 : 256);
+  const int64_t feat = (q.N + fn::kMgFeat - 1) / fn::kMgFeat;
+  // experts can own a partly filled tile each
+  const int64_t most = feat * ((q.M + k.tok - 1) / k.tok + (grouped ? std::min(q.E, q.M) : 0));
+  if (most > INT32_MAX / 2) return FN_ERR_UNSUPPORTED;
+  p.box = q.rows ? 1 : std::min(k.tok, 64);
+  CUtensorMap x_map, w_map;
+  if (!code_map(&x_map, q.a_q, q.a_rows, q.K, p.box) ||
+      !code_map(&w_map, q.b_q, p.E * q.N, q.K, fn::kMgFeat))
+    return FN_ERR_CUDA;
+  const int smem = k.smem + (grouped ? (3 * p.E + 1) * 4 : 0);
+  if (!allow_smem(reinterpret_cast<const void*>(k.kernel), smem)) return FN_ERR_CUDA;
+  const unsigned grid = (unsigned)std::min<int64_t>(most, sms);
+  const int st = launch(k.kernel, grid, fn::kMgThreads, smem, stream, 1, p, x_map, w_map);
+  if (st == FN_OK) record(MX_VARIANT_GEMM, grid, fn::kMgThreads, k.tok, 1);
+  return st;
+}
+
+// ---- silu_mul_quant ---------------------------------------------------------------------
+
+struct ModeInfo {
+  int q = -1, layout = 0;
+  bool f16 = false;
+};
+
+int parse_mode(int mode, ModeInfo* mi) {
+  const int q = mode & FN_MODE_MASK, flags = mode & ~(FN_MODE_MASK | FN_IO_FP16);
+  if (q < FN_FP8_PER_TOKEN || q > FN_MXFP4) return FN_ERR_INVALID;
+  mi->q = q;
+  mi->f16 = (mode & FN_IO_FP16) != 0;
+  mi->layout = fn::SCALE_ROW_MAJOR;
+  if (flags == FN_SCALE_SWIZZLE_32_4_4 && q == FN_MXFP4)
+    mi->layout = fn::SCALE_SWIZZLE_32_4_4;
+  else if (flags == FN_SCALE_MN_MAJOR && q == FN_FP8_PER_GROUP128)
+    mi->layout = fn::SCALE_MN_MAJOR;
+  else if (flags != 0)
+    return FN_ERR_INVALID;
+  return FN_OK;
+}
+
+template <int MODE>
+fn::ActKernel act_groups(bool f16) {
+  return f16 ? fn::act_groups_kernel<MODE, fn::F16> : fn::act_groups_kernel<MODE, fn::Bf16>;
+}
+
+template <class IO>
+fn::ActKernel act_row(int V) {
+  return V == 1   ? fn::act_row_kernel<1, IO>
+         : V == 2 ? fn::act_row_kernel<2, IO>
+                  : fn::act_row_kernel<4, IO>;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_version(void) { return 100; }
+
+int mx_last_variant(void) { return tl_variant; }
+
+void mx_last_launch(int32_t out[4]) {
+  if (out) std::memcpy(out, tl_launch, sizeof tl_launch);
+}
+
+int mx_programmatic_launch(int on) {
+  const int old = tl_pdl;
+  tl_pdl = on ? 1 : 0;
+  return old;
+}
+
+const char* mx_status_string(int status) {
+  switch (status) {
+    case FN_OK: return "ok";
+    case FN_ERR_INVALID: return "invalid argument (null pointer, size, flag or overlap)";
+    case FN_ERR_ALIGN: return "misaligned pointer or stride";
+    case FN_ERR_UNSUPPORTED: return "shape outside the built kernels";
+    case FN_ERR_CUDA: return "CUDA launch failed";
+    default: return "unknown status";
+  }
+}
+
+int mx_gemm(const void* a_q, const void* a_scale, const void* b_q, const void* b_scale, int64_t M,
+            int64_t N, int64_t K, int flags, void* out, int64_t ldo, void* stream) {
+  tl_variant = MX_VARIANT_NONE;
+  const Product q = {a_q, a_scale, b_q, b_scale, nullptr, nullptr, M, 1, M, N, K, ldo, flags, out};
+  if (int st = check_product(q, false)) return st;
+  if (M == 0) return FN_OK;
+  if (int st = check_product_pointers(q, false)) return st;
+  return launch_product(q, false, stream);
+}
+
+int mx_grouped_gemm(const void* a_q, const void* a_scale, int64_t a_rows, const int32_t* rows,
+                    const int32_t* offsets, int64_t E, const void* b_q, const void* b_scale,
+                    int64_t R, int64_t N, int64_t K, int flags, void* out, int64_t ldo,
+                    void* stream) {
+  tl_variant = MX_VARIANT_NONE;
+  const Product q = {a_q,    a_scale, b_q, b_scale, rows, offsets, a_rows,
+                     E,      R,       N,   K,       ldo,  flags,   out};
+  if (int st = check_product(q, true)) return st;
+  if (R == 0) return FN_OK;
+  if (int st = check_product_pointers(q, true)) return st;
+  return launch_product(q, true, stream);
+}
+
+int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H,
+                      const int32_t* num_rows, void* out_q, void* out_scale, void* out_y,
+                      void* stream) {
+  tl_variant = MX_VARIANT_NONE;
+  ModeInfo mi;
+  if (int st = parse_mode(mode, &mi)) return st;
+  if (M < 0 || H <= 0 || H % 8 || ldx < 2 * H) return FN_ERR_INVALID;
+  if (mi.q == FN_FP8_PER_GROUP128 && H % 128) return FN_ERR_INVALID;
+  if (mi.q == FN_MXFP4 && H % 32) return FN_ERR_INVALID;
+  if (H > FN_MAX_H || M > (int64_t)INT32_MAX / 8 || ldx > ((int64_t)1 << 31))
+    return FN_ERR_UNSUPPORTED;
+  if (M == 0) return FN_OK;
+  if (!x || !out_q || !out_scale) return FN_ERR_INVALID;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(out_y, 16) || !aligned(num_rows, 4) ||
+      !aligned(out_q, mi.q == FN_MXFP4 ? 4 : 8) || (mi.q != FN_MXFP4 && !aligned(out_scale, 4)))
+    return FN_ERR_ALIGN;
+  const int64_t sb = mi.q == FN_FP8_PER_TOKEN ? M * 4
+                     : mi.q == FN_FP8_PER_GROUP128
+                         ? (mi.layout == fn::SCALE_MN_MAJOR ? round_up(M, 4) : M) * (H / 128) * 4
+                         : scale_bytes(M, H, mi.layout == fn::SCALE_SWIZZLE_32_4_4);
+  const Range in[2] = {range_of(x, ((M - 1) * ldx + 2 * H) * 2),
+                       range_of(num_rows, num_rows ? 4 : 0)};
+  const Range outs[3] = {range_of(out_q, mi.q == FN_MXFP4 ? M * H / 2 : M * H),
+                         range_of(out_scale, sb), range_of(out_y, out_y ? M * H * 2 : 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : in)
+      if (overlap(outs[i], r)) return FN_ERR_INVALID;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return FN_ERR_INVALID;
+  }
+  fn::ActParams p;
+  std::memset(&p, 0, sizeof p);
+  p.x = static_cast<const uint4*>(x);
+  p.num_rows = num_rows;
+  p.out_q = static_cast<uint8_t*>(out_q);
+  p.out_scale = out_scale;
+  p.out_y = static_cast<uint4*>(out_y);
+  p.M = M;
+  p.ldv = ldx / 8;
+  p.nvec = (int)(H / 8);
+  p.scale_layout = mi.layout;
+  p.scale_ld = mi.layout == fn::SCALE_SWIZZLE_32_4_4 ? round_up(H / 32, 4) / 4
+               : mi.layout == fn::SCALE_MN_MAJOR     ? round_up(M, 4)
+                                                     : 0;
+  const int sms = sm_count();
+  if (sms <= 0) return FN_ERR_CUDA;
+  if (mi.q == FN_FP8_PER_TOKEN) {
+    const int V = p.nvec <= 1024 ? 1 : p.nvec <= 2048 ? 2 : 4;
+    const unsigned threads = (unsigned)round_up((p.nvec + V - 1) / V, 32);
+    const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sms * 64);
+    const int st = launch(mi.f16 ? act_row<fn::F16>(V) : act_row<fn::Bf16>(V), grid, threads, 0,
+                          stream, 1, p);
+    if (st == FN_OK) record(MX_VARIANT_SILU_ROW, grid, threads, V, 1);
+    return st;
+  }
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((M * p.nvec + 255) / 256, (int64_t)sms * 64);
+  const int st = launch(mi.q == FN_MXFP4 ? act_groups<fn::MODE_MX>(mi.f16)
+                                         : act_groups<fn::MODE_G128>(mi.f16),
+                        grid, 256, 0, stream, 1, p);
+  if (st == FN_OK) record(MX_VARIANT_SILU_GROUPS, grid, 256, 1, 1);
+  return st;
+}
+
+int mx_combine(const void* y, int64_t R, const int32_t* pos, const float* weight, const void* base,
+               int64_t T, int k, int64_t N, int flags, void* out, void* stream) {
+  tl_variant = MX_VARIANT_NONE;
+  if (flags & ~FN_IO_FP16) return FN_ERR_INVALID;
+  if (T < 0 || R < 0 || k < 0 || N < 1) return FN_ERR_INVALID;
+  if (k > MX_MAX_TOP || N > (1 << 24) || R > INT32_MAX) return FN_ERR_UNSUPPORTED;
+  const bool f16 = (flags & FN_IO_FP16) != 0;
+  if (T > INT32_MAX || T * ((N + 255) / 256) > INT32_MAX) return FN_ERR_UNSUPPORTED;  // grid size
+  if (T == 0) return FN_OK;
+  if (!out || (k > 0 && (!pos || !weight)) || (k > 0 && R > 0 && !y)) return FN_ERR_INVALID;
+  if (!aligned(y, 2) || !aligned(base, 2) || !aligned(out, 2) || !aligned(pos, 4) ||
+      !aligned(weight, 4))
+    return FN_ERR_ALIGN;
+  const Range o = range_of(out, T * N * 2);
+  if (overlap(o, range_of(y, R * N * 2)) || overlap(o, range_of(pos, T * k * 4)) ||
+      overlap(o, range_of(weight, T * k * 4)) ||
+      (base && base != out && overlap(o, range_of(base, T * N * 2))))
+    return FN_ERR_INVALID;
+  const bool wide = N % 8 == 0 && aligned(y, 16) && aligned(base, 16) && aligned(out, 16);
+  fn::CombineParams p;
+  std::memset(&p, 0, sizeof p);
+  p.y = y;
+  p.pos = pos;
+  p.weight = weight;
+  p.base = base;
+  p.out = out;
+  p.R = R;
+  p.T = T;
+  p.k = k;
+  p.n = (int)(wide ? N / 8 : N);
+  const unsigned threads = (unsigned)std::min<int64_t>(256, round_up(p.n, 32));
+  p.per_row = (p.n + (int)threads - 1) / (int)threads;
+  const unsigned grid = (unsigned)(T * p.per_row);
+  fn::CombineKernel kern = wide ? (f16 ? fn::combine_kernel<fn::F16> : fn::combine_kernel<fn::Bf16>)
+                                : (f16 ? fn::combine_narrow_kernel<fn::F16>
+                                       : fn::combine_narrow_kernel<fn::Bf16>);
+  const int st = launch(kern, grid, threads, 0, stream, 1, p);
+  if (st == FN_OK)
+    record(wide ? MX_VARIANT_COMBINE : MX_VARIANT_COMBINE_NARROW, grid, threads, 1, 1);
+  return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,45 @@
+// Parameter block and instance table of the MXFP4 product kernels
+// (mg_kernel.cuh), shared by the host dispatch and the instantiation unit.
+#pragma once
+#include <cuda.h>
+
+#include <cstdint>
+
+namespace fn {
+
+enum : int { MG_OUT_BF16 = 0, MG_OUT_FP16 = 1, MG_OUT_FP32 = 2 };
+
+constexpr int kMgFeat = 128;         // output features of a tile (the MMA's M)
+constexpr int kMgStageK = 256;       // elements of a K step (128 bytes of codes a row)
+constexpr int kMgThreads = 256;      // 4 role warps, 4 epilogue warps
+constexpr int kMgMaxExperts = 1024;  // the tile table in shared memory
+
+struct MGParams {
+  const uint8_t* x_scale;   // token rows' scales
+  const uint8_t* w_scale;   // weights' scales
+  void* out;
+  const int32_t* offsets;   // [E + 1] row ranges of the experts, or nullptr (one product)
+  const int32_t* rows;      // source row of each row, or nullptr
+  int64_t ldo;              // row stride of out, elements
+  int64_t w_scale_stride;   // bytes of one expert's weight scales
+  int M;                    // rows (of out)
+  int x_rows;               // rows of the token operand
+  int N, K, E;
+  int groups;               // K / 32
+  int x_swizzled, w_swizzled;
+  int out_type;
+  int box;                  // rows of a token TMA box (1: gather)
+};
+
+using MGKernel = void (*)(const MGParams, const CUtensorMap, const CUtensorMap);
+
+struct MGInstance {
+  MGKernel kernel;
+  int tok;       // token rows of a tile
+  int smem;      // dynamic shared memory without the tile table
+};
+
+// The instance for a token tile of `tok` rows (16, 64, 128 or 256).
+MGInstance mg_pick(int tok);
+
+}  // namespace fn
