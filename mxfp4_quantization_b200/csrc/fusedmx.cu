@@ -112,6 +112,19 @@ EncodeTiled encoder() {
   return f;
 }
 
+// Scale tiles of the 32x4x4 tiling, 512 bytes each; boxes of two.
+bool scale_map(CUtensorMap* m, const void* s, int64_t tiles) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)tiles};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t boxes[2] = {128, 2};
+  const cuuint32_t elem[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(s), dims, strides, boxes,
+             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Code rows [rows, K/2] bytes; boxes of 128 bytes x `box` rows, swizzled.
 bool code_map(CUtensorMap* m, const void* q, int64_t rows, int64_t K, int box) {
   EncodeTiled enc = encoder();
@@ -220,27 +233,37 @@ int launch_product(const Product& q, bool grouped, void* stream) {
   p.K = (int)q.K;
   p.E = grouped ? (int)q.E : 1;
   p.groups = (int)(q.K / 32);
-  p.x_swizzled = q.flags & MX_A_SCALE_SWIZZLE ? 1 : 0;
-  p.w_swizzled = q.flags & MX_B_SCALE_SWIZZLE ? 1 : 0;
+  // an odd number of groups: the last MMA reads a byte of the tiling's padding
+  const int tiled = p.groups & 1 ? fn::MG_SCALE_TMA_TAIL : fn::MG_SCALE_TMA;
+  p.x_mode = q.flags & MX_A_SCALE_SWIZZLE ? tiled : fn::MG_SCALE_WARP;
+  p.w_mode = q.flags & MX_B_SCALE_SWIZZLE ? tiled : fn::MG_SCALE_WARP;
+  p.x_wide = p.groups % 16 == 0 && aligned(q.a_scale, 16);
+  p.w_wide = p.groups % 16 == 0 && aligned(q.b_scale, 16);
   p.out_type = q.flags & 0xF;
+  p.out_quads = p.out_type != MX_OUT_FP32 && q.N % 4 == 0 && q.ldo % 4 == 0 && aligned(q.out, 8);
   const int sms = sm_count();
   if (sms <= 0) return FN_ERR_CUDA;
   const int64_t each = grouped ? (q.M + q.E - 1) / q.E : q.M;
   const fn::MGInstance k = fn::mg_pick(each <= 16 ? 16 : each <= 64 ? 64 : each <= 128 ? 128 : 256);
-  const int64_t feat = (q.N + fn::kMgFeat - 1) / fn::kMgFeat;
+  const int64_t feat = (q.N + k.pair * fn::kMgFeat - 1) / (k.pair * fn::kMgFeat);
   // experts can own a partly filled tile each
   const int64_t most = feat * ((q.M + k.tok - 1) / k.tok + (grouped ? std::min(q.E, q.M) : 0));
-  if (most > INT32_MAX / 2) return FN_ERR_UNSUPPORTED;
-  p.box = q.rows ? 1 : std::min(k.tok, 64);
-  CUtensorMap x_map, w_map;
-  if (!code_map(&x_map, q.a_q, q.a_rows, q.K, p.box) ||
-      !code_map(&w_map, q.b_q, p.E * q.N, q.K, fn::kMgFeat))
+  const int64_t tiles_w = scale_bytes(q.N, q.K, true) / 512 * p.E,
+                tiles_x = scale_bytes(q.a_rows, q.K, true) / 512;
+  if (most > INT32_MAX / 2 || tiles_w > kMaxRows || tiles_x > kMaxRows) return FN_ERR_UNSUPPORTED;
+  p.box = q.rows ? 1 : std::min(k.tok / k.pair, 64);
+  fn::MGMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  if (!code_map(&maps.x, q.a_q, q.a_rows, q.K, p.box) ||
+      !code_map(&maps.w, q.b_q, p.E * q.N, q.K, fn::kMgFeat) ||
+      (p.x_mode != fn::MG_SCALE_WARP && !scale_map(&maps.xs, q.a_scale, tiles_x)) ||
+      (p.w_mode != fn::MG_SCALE_WARP && !scale_map(&maps.ws, q.b_scale, tiles_w)))
     return FN_ERR_CUDA;
   const int smem = k.smem + (grouped ? (3 * p.E + 1) * 4 : 0);
   if (!allow_smem(reinterpret_cast<const void*>(k.kernel), smem)) return FN_ERR_CUDA;
-  const unsigned grid = (unsigned)std::min<int64_t>(most, sms);
-  const int st = launch(k.kernel, grid, fn::kMgThreads, smem, stream, 1, p, x_map, w_map);
-  if (st == FN_OK) record(MX_VARIANT_GEMM, grid, fn::kMgThreads, k.tok, 1);
+  const unsigned grid = (unsigned)(std::min<int64_t>(most, sms / k.pair) * k.pair);
+  const int st = launch(k.kernel, grid, fn::kMgThreads, smem, stream, k.pair, p, maps);
+  if (st == FN_OK) record(MX_VARIANT_GEMM, grid, fn::kMgThreads, k.tok, k.pair);
   return st;
 }
 

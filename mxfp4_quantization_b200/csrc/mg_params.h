@@ -9,9 +9,16 @@ namespace fn {
 
 enum : int { MG_OUT_BF16 = 0, MG_OUT_FP16 = 1, MG_OUT_FP32 = 2 };
 
-constexpr int kMgFeat = 128;         // output features of a tile (the MMA's M)
+// Who brings an operand's scales to shared memory.
+enum : int {
+  MG_SCALE_TMA = 0,       // TMA boxes of the 32x4x4 tiling
+  MG_SCALE_TMA_TAIL = 1,  // the same, but the last K step by a warp (it masks padding)
+  MG_SCALE_WARP = 2,      // a warp, from row-major bytes
+};
+
+constexpr int kMgFeat = 128;         // output features of a block's tile
 constexpr int kMgStageK = 256;       // elements of a K step (128 bytes of codes a row)
-constexpr int kMgThreads = 256;      // 4 role warps, 4 epilogue warps
+constexpr int kMgThreads = 288;      // 5 role warps, 4 epilogue warps
 constexpr int kMgMaxExperts = 1024;  // the tile table in shared memory
 
 struct MGParams {
@@ -26,20 +33,28 @@ struct MGParams {
   int x_rows;               // rows of the token operand
   int N, K, E;
   int groups;               // K / 32
-  int x_swizzled, w_swizzled;
+  int x_mode, w_mode;       // MG_SCALE_*
+  int x_wide, w_wide;       // row-major scale rows are whole aligned 16-byte vectors
   int out_type;
+  int out_quads;            // 16-bit output whose rows are whole aligned groups of 4
   int box;                  // rows of a token TMA box (1: gather)
 };
 
-using MGKernel = void (*)(const MGParams, const CUtensorMap, const CUtensorMap);
+struct MGMaps {
+  CUtensorMap x, w;        // codes
+  CUtensorMap xs, ws;      // scale tiles (512 bytes each), where a TMA mode reads them
+};
+
+using MGKernel = void (*)(const MGParams, const MGMaps);
 
 struct MGInstance {
   MGKernel kernel;
   int tok;       // token rows of a tile
+  int pair;      // blocks that share a tile (cta_group)
   int smem;      // dynamic shared memory without the tile table
 };
 
-// The instance for a token tile of `tok` rows (16, 64, 128 or 256).
+// The instance for a token tile of `tok` rows (16, 64, 128, or 256 over a pair).
 MGInstance mg_pick(int tok);
 
 }  // namespace fn
