@@ -13,8 +13,10 @@
  *  - Every data pointer is a DEVICE pointer owned by the caller, memory of the
  *    current device.  The library allocates nothing and never synchronizes: work
  *    is queued on `stream` (a cudaStream_t passed as void*; NULL means the legacy
- *    default stream).  No workspace: calls on any number of streams, threads and
- *    captured graphs are independent of each other.
+ *    default stream).  A call that needs a workspace takes it from the caller (the
+ *    *_workspace_bytes functions give its size, 0 where none is needed); it may
+ *    be reused as soon as the call's work on `stream` is done, so calls that can
+ *    overlap on the GPU (different streams, concurrent graphs) need one each.
  *  - All argument checks run on the host before anything is launched; on any error
  *    nothing is launched and no output is touched.  A call without rows returns
  *    FN_OK and launches nothing once the sizes and flags are valid; the data
@@ -69,14 +71,21 @@ extern "C" {
  * out      [M, N] of the output type, rows ldo elements apart (ldo >= N, at most
  *          2^28; more is FN_ERR_UNSUPPORTED).
  *          Elements between N and ldo are not written.
- * Alignment  a_q and b_q 16 bytes; swizzled scales 16 bytes; out its element
- *          size.  Otherwise FN_ERR_ALIGN.  Padding of swizzled scales is not
- *          used whatever it holds.
- * Overlap  out must not overlap an input (FN_ERR_INVALID).
+ * workspace  device memory of mx_gemm_workspace_bytes(M, N, K, flags) bytes,
+ *          or NULL where that is 0.
+ * Alignment  a_q and b_q 16 bytes; swizzled scales and the workspace 16 bytes;
+ *          out its element size.  Otherwise FN_ERR_ALIGN.  Padding of swizzled
+ *          scales is not used whatever it holds.
+ * Overlap  out and workspace must not overlap each other or an input
+ *          (FN_ERR_INVALID).
  */
 FN_API int mx_gemm(const void* a_q, const void* a_scale, const void* b_q, const void* b_scale,
                    int64_t M, int64_t N, int64_t K, int flags, void* out, int64_t ldo,
-                   void* stream);
+                   void* workspace, void* stream);
+
+/* Bytes of workspace mx_gemm needs for these sizes and flags, or -1 where the
+ * call would refuse them. */
+FN_API int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int flags);
 
 /*
  * The product with one weight for each of E experts over ragged row ranges:
@@ -92,19 +101,24 @@ FN_API int mx_gemm(const void* a_q, const void* a_scale, const void* b_q, const 
  * rows     int32 [R] or NULL (then a_rows >= R).  A row whose index is outside
  *          [0, a_rows) gives a row of zeros.  An index may occur any number
  *          of times.
- * offsets  int32 [E + 1], non-decreasing, in [0, R].  Values outside are
- *          clamped into [0, R], and a range that runs backwards is empty;
- *          where ranges overlap, the rows hold one of the owners' results.
+ * offsets  int32 [E + 1], non-decreasing, in [0, R].  Other values break the
+ *          contract: the rows of out then hold unspecified values, and no
+ *          other memory is touched.
  * b_q      u8 [E, N, K/2];  b_scale [E, N, K/32], or swizzled: E tilings of
  *          roundup(N,128) * roundup(K/32,4) bytes, one after another.
  * R        rows of out, >= 0.  E: 1..MX_MAX_EXPERTS (above: FN_ERR_UNSUPPORTED).
  * Other arguments, alignment (offsets and rows 4 bytes), overlap and limits
- * as mx_gemm.
+ * as mx_gemm; the workspace has mx_grouped_gemm_workspace_bytes bytes.
  */
 FN_API int mx_grouped_gemm(const void* a_q, const void* a_scale, int64_t a_rows,
                            const int32_t* rows, const int32_t* offsets, int64_t E,
                            const void* b_q, const void* b_scale, int64_t R, int64_t N, int64_t K,
-                           int flags, void* out, int64_t ldo, void* stream);
+                           int flags, void* out, int64_t ldo, void* workspace, void* stream);
+
+/* Bytes of workspace mx_grouped_gemm needs (gather != 0: called with `rows`), or
+ * -1 where the call would refuse the sizes or flags. */
+FN_API int64_t mx_grouped_gemm_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K,
+                                               int flags, int gather);
 
 /*
  * Gated activation and quantization of its result, one pass over the rows:
@@ -152,11 +166,13 @@ FN_API int mx_combine(const void* y, int64_t R, const int32_t* pos, const float*
  * after an error or a call without rows). */
 typedef enum {
     MX_VARIANT_NONE = 0,
-    MX_VARIANT_GEMM = 1,          /* mx_gemm, mx_grouped_gemm: one block per tile        */
+    MX_VARIANT_GEMM = 1,          /* products of few rows: one block per tile, or a
+                                     cluster of blocks that share a tile's K steps      */
     MX_VARIANT_SILU_GROUPS = 2,   /* mx_silu_mul_quant, group modes                     */
     MX_VARIANT_SILU_ROW = 3,      /* mx_silu_mul_quant, per-token mode                   */
     MX_VARIANT_COMBINE = 4,       /* mx_combine, 16-byte vectors                         */
-    MX_VARIANT_COMBINE_NARROW = 5 /* mx_combine, single elements                         */
+    MX_VARIANT_COMBINE_NARROW = 5, /* mx_combine, single elements                        */
+    MX_VARIANT_GEMM_PAIR = 6      /* products of many rows: pairs of blocks per tile     */
 } mx_variant;
 FN_API int mx_last_variant(void);
 

@@ -47,9 +47,11 @@ int sm_count() {
   return n;
 }
 
+// `pdl`: as a programmatic dependent of the work before it on the stream (every
+// kernel waits for that work before it touches memory).
 template <typename... KArgs, typename... Args>
 int launch(void (*k)(KArgs...), unsigned grid, unsigned threads, size_t smem, void* stream,
-           int cluster, const Args&... args) {
+           int cluster, bool pdl, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -64,7 +66,7 @@ int launch(void (*k)(KArgs...), unsigned grid, unsigned threads, size_t smem, vo
     attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (tl_pdl) {
+  if (pdl) {
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n].val.programmaticStreamSerializationAllowed = 1;
     ++n;
@@ -165,6 +167,7 @@ struct Product {
   int64_t a_rows, E, M, N, K, ldo;
   int flags;
   void* out;
+  void* workspace;
 };
 
 constexpr int64_t kMaxRows = INT32_MAX - 256;  // row coordinates with a tile's reach on top
@@ -192,32 +195,92 @@ int check_product(const Product& q, bool grouped) {
   return FN_OK;
 }
 
-int check_product_pointers(const Product& q, bool grouped) {
+int check_product_pointers(const Product& q, bool grouped, int64_t ws_bytes) {
   if (!q.a_q || !q.a_scale || !q.b_q || !q.b_scale || !q.out) return FN_ERR_INVALID;
+  if (ws_bytes > 0 && !q.workspace) return FN_ERR_INVALID;
   if (grouped && !q.offsets) return FN_ERR_INVALID;
   if (grouped && (q.rows ? q.a_rows < 1 : q.a_rows < q.M)) return FN_ERR_INVALID;
-  if (!aligned(q.a_q, 16) || !aligned(q.b_q, 16) || !aligned(q.out, out_size(q.flags)))
+  if (!aligned(q.a_q, 16) || !aligned(q.b_q, 16) || !aligned(q.out, out_size(q.flags)) ||
+      (ws_bytes > 0 && !aligned(q.workspace, 16)))
     return FN_ERR_ALIGN;
   if ((q.flags & MX_A_SCALE_SWIZZLE && !aligned(q.a_scale, 16)) ||
       (q.flags & MX_B_SCALE_SWIZZLE && !aligned(q.b_scale, 16)))
     return FN_ERR_ALIGN;
   if (grouped && (!aligned(q.offsets, 4) || !aligned(q.rows, 4))) return FN_ERR_ALIGN;
-  const Range out = range_of(q.out, ((q.M - 1) * q.ldo + q.N) * out_size(q.flags));
   const int64_t E = grouped ? q.E : 1;
-  const int64_t b_scale = E * scale_bytes(q.N, q.K, q.flags & MX_B_SCALE_SWIZZLE);
-  if (overlap(out, range_of(q.a_q, q.a_rows * q.K / 2)) ||
-      overlap(out, range_of(q.a_scale,
-                            scale_bytes(q.a_rows, q.K, q.flags & MX_A_SCALE_SWIZZLE))) ||
-      overlap(out, range_of(q.b_q, E * q.N * q.K / 2)) ||
-      overlap(out, range_of(q.b_scale, b_scale)))
-    return FN_ERR_INVALID;
-  if (grouped && (overlap(out, range_of(q.offsets, (q.E + 1) * 4)) ||
-                  (q.rows && overlap(out, range_of(q.rows, q.M * 4)))))
-    return FN_ERR_INVALID;
+  const Range in[6] = {
+      range_of(q.a_q, q.a_rows * q.K / 2),
+      range_of(q.a_scale, scale_bytes(q.a_rows, q.K, q.flags & MX_A_SCALE_SWIZZLE)),
+      range_of(q.b_q, E * q.N * q.K / 2),
+      range_of(q.b_scale, E * scale_bytes(q.N, q.K, q.flags & MX_B_SCALE_SWIZZLE)),
+      range_of(q.offsets, grouped ? (q.E + 1) * 4 : 0),
+      range_of(q.rows, q.rows ? q.M * 4 : 0)};
+  const Range out = range_of(q.out, ((q.M - 1) * q.ldo + q.N) * out_size(q.flags));
+  const Range ws = range_of(q.workspace, ws_bytes);
+  for (const Range& r : in)
+    if (overlap(out, r) || (ws_bytes > 0 && overlap(ws, r))) return FN_ERR_INVALID;
+  if (ws_bytes > 0 && overlap(ws, out)) return FN_ERR_INVALID;
   return FN_OK;
 }
 
-int launch_product(const Product& q, bool grouped, void* stream) {
+// How a product runs: a function of its sizes and flags alone, so that the
+// workspace query and the call agree.
+struct Plan {
+  bool pair = false;
+  int tok = 0;             // rows of a tile
+  int split = 1;           // single-block kernel: blocks that share a tile's K steps
+  int64_t feat = 0;        // feature tiles
+  int64_t pieces = 0;      // row tiles, at most
+  int64_t x_bytes = 0, w_bytes = 0, code_bytes = 0;  // workspace
+  int64_t workspace() const { return x_bytes + w_bytes + code_bytes; }
+};
+
+constexpr int kSms = 148;  // B200
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// `gather`: rows by index.  FN_ERR_UNSUPPORTED beyond the kernels' index range.
+int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool grouped, bool gather,
+                 Plan* out) {
+  Plan p;
+  const int64_t each = grouped ? ceil_div(M, E) : M;
+  const int64_t more = grouped ? std::min(E, M) : 0;  // a partly filled tile an expert
+  const int64_t groups = K / 32, kts = ceil_div(groups, 4);
+  p.pair = each > 128;
+  if (p.pair) {
+    p.feat = ceil_div(N, fn::kMgPairFeat);
+    p.tok = fn::kMgPairRows;
+    if (!grouped) {
+      // the tile height with the least rows times waves of pairs; a tile also costs
+      // about as much as 32 more rows (its weights, its epilogue)
+      int64_t best = INT64_MAX;
+      for (int tok = fn::kMgPairRows; tok >= 48; tok -= 16) {
+        const int64_t cost = ceil_div(ceil_div(M, tok) * p.feat, kSms / 2) * (tok + 32);
+        if (cost < best) best = cost, p.tok = tok;
+      }
+    }
+    p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
+    p.x_bytes = p.pieces * 2 * kts * 512;
+    // weights' tiles are taken as they are, unless a padding byte would be read
+    if (!(flags & MX_B_SCALE_SWIZZLE) || groups & 1)
+      p.w_bytes = (grouped ? E : 1) * ceil_div(N, 128) * kts * 512;
+    if (gather) p.code_bytes = M * (K / 2);
+  } else {
+    p.feat = ceil_div(N, fn::kMgFeat);
+    p.tok = each <= 16 ? 16 : each <= 64 ? 64 : 128;
+    p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
+    // few tiles: the blocks of a cluster share the K steps of one
+    const int64_t steps = ceil_div(K, fn::kMgStageK), tiles = p.feat * p.pieces;
+    while (p.split < 8 && tiles * p.split * 2 <= 2 * kSms && p.split * 4 <= steps) p.split *= 2;
+  }
+  if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * 2 * kts > kMaxRows ||
+      (grouped ? E : 1) * ceil_div(N, 128) * kts > kMaxRows || ceil_div(M, 128) * kts > kMaxRows)
+    return FN_ERR_UNSUPPORTED;
+  *out = p;
+  return FN_OK;
+}
+
+int launch_product(const Product& q, bool grouped, const Plan& plan, void* stream) {
   fn::MGParams p;
   std::memset(&p, 0, sizeof p);
   p.x_scale = static_cast<const uint8_t*>(q.a_scale);
@@ -241,30 +304,80 @@ int launch_product(const Product& q, bool grouped, void* stream) {
   p.w_wide = p.groups % 16 == 0 && aligned(q.b_scale, 16);
   p.out_type = q.flags & 0xF;
   p.out_quads = p.out_type != MX_OUT_FP32 && q.N % 4 == 0 && q.ldo % 4 == 0 && aligned(q.out, 8);
+  p.tok = plan.tok;
+  p.pieces = (int)plan.pieces;
+  p.split = plan.split;
   const int sms = sm_count();
   if (sms <= 0) return FN_ERR_CUDA;
-  const int64_t each = grouped ? (q.M + q.E - 1) / q.E : q.M;
-  const fn::MGInstance k = fn::mg_pick(each <= 16 ? 16 : each <= 64 ? 64 : each <= 128 ? 128 : 256);
-  const int64_t feat = (q.N + k.pair * fn::kMgFeat - 1) / (k.pair * fn::kMgFeat);
-  // experts can own a partly filled tile each
-  const int64_t most = feat * ((q.M + k.tok - 1) / k.tok + (grouped ? std::min(q.E, q.M) : 0));
-  const int64_t tiles_w = scale_bytes(q.N, q.K, true) / 512 * p.E,
-                tiles_x = scale_bytes(q.a_rows, q.K, true) / 512;
-  if (most > INT32_MAX / 2 || tiles_w > kMaxRows || tiles_x > kMaxRows) return FN_ERR_UNSUPPORTED;
-  p.box = q.rows ? 1 : std::min(k.tok / k.pair, 64);
+  const int table = grouped ? (3 * p.E + 1) * 4 : 0;
+  const int64_t tiles_w = p.E * ceil_div(q.N, 128) * ceil_div(p.groups, 4);
+  const int64_t tiles_x = ceil_div(q.a_rows, 128) * ceil_div(p.groups, 4);
+  const fn::MGInstance k = plan.pair ? fn::mg_pair() : fn::mg_pick(plan.tok);
   fn::MGMaps maps;
   std::memset(&maps, 0, sizeof maps);
-  if (!code_map(&maps.x, q.a_q, q.a_rows, q.K, p.box) ||
-      !code_map(&maps.w, q.b_q, p.E * q.N, q.K, fn::kMgFeat) ||
-      (p.x_mode != fn::MG_SCALE_WARP && !scale_map(&maps.xs, q.a_scale, tiles_x)) ||
-      (p.w_mode != fn::MG_SCALE_WARP && !scale_map(&maps.ws, q.b_scale, tiles_w)))
+  if (!code_map(&maps.w, q.b_q, p.E * q.N, q.K, fn::kMgFeat) ||
+      !allow_smem(reinterpret_cast<const void*>(k.kernel), k.smem + table))
     return FN_ERR_CUDA;
-  const int smem = k.smem + (grouped ? (3 * p.E + 1) * 4 : 0);
-  if (!allow_smem(reinterpret_cast<const void*>(k.kernel), smem)) return FN_ERR_CUDA;
-  const unsigned grid = (unsigned)(std::min<int64_t>(most, sms / k.pair) * k.pair);
-  const int st = launch(k.kernel, grid, fn::kMgThreads, smem, stream, k.pair, p, maps);
-  if (st == FN_OK) record(MX_VARIANT_GEMM, grid, fn::kMgThreads, k.tok, k.pair);
+  if (!plan.pair) {
+    p.box = q.rows ? 1 : std::min(plan.tok, 64);
+    if (!code_map(&maps.x, q.a_q, q.a_rows, q.K, p.box) ||
+        (p.x_mode != fn::MG_SCALE_WARP && !scale_map(&maps.xs, q.a_scale, tiles_x)) ||
+        (p.w_mode != fn::MG_SCALE_WARP && !scale_map(&maps.ws, q.b_scale, tiles_w)))
+      return FN_ERR_CUDA;
+    const int64_t tiles = plan.feat * plan.pieces;
+    const unsigned grid = (unsigned)(plan.split > 1
+                                         ? tiles * plan.split
+                                         : std::min<int64_t>(tiles, (int64_t)sms * k.per_sm));
+    const int st = launch(k.kernel, grid, fn::kMgThreads, k.smem + table, stream, plan.split,
+                          tl_pdl != 0, p, maps);
+    if (st == FN_OK) record(MX_VARIANT_GEMM, grid, fn::kMgThreads, plan.tok, plan.split);
+    return st;
+  }
+  fn::MGArrange a;
+  std::memset(&a, 0, sizeof a);
+  uint8_t* ws = static_cast<uint8_t*>(q.workspace);
+  a.x_tiles = ws;
+  a.w_tiles = plan.w_bytes ? ws + plan.x_bytes : nullptr;
+  a.codes = plan.code_bytes ? reinterpret_cast<uint4*>(ws + plan.x_bytes + plan.w_bytes) : nullptr;
+  a.x_codes = static_cast<const uint4*>(q.a_q);
+  a.x_swizzled = q.flags & MX_A_SCALE_SWIZZLE ? 1 : 0;
+  a.w_swizzled = q.flags & MX_B_SCALE_SWIZZLE ? 1 : 0;
+  p.box = fn::kMgPairRows / 6;
+  if (!code_map(&maps.x, a.codes ? static_cast<const void*>(a.codes) : q.a_q,
+                a.codes ? q.M : q.a_rows, q.K, p.box) ||
+      !scale_map(&maps.xs, a.x_tiles, plan.x_bytes / 512) ||
+      !scale_map(&maps.ws, a.w_tiles ? a.w_tiles : q.b_scale, tiles_w))
+    return FN_ERR_CUDA;
+  const int64_t items = std::max(plan.pieces * 2, a.w_tiles ? p.E * ceil_div(q.N, 128) : 0) *
+                        ceil_div(ceil_div(p.groups, 4), 4);
+  const int64_t blocks =
+      std::max(ceil_div(items, 8), a.codes ? ceil_div(q.M * p.groups, 1024) : 0);
+  const unsigned agrid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
+  if (launch(fn::mg_arrange(), agrid, 256, table, stream, 1, tl_pdl != 0, p, a) != FN_OK)
+    return FN_ERR_CUDA;
+  const unsigned grid = (unsigned)(std::min<int64_t>(plan.feat * plan.pieces, sms / 2) * 2);
+  const int st = launch(k.kernel, grid, fn::kMgPairThreads, k.smem + table, stream, 2, true, p, maps);
+  if (st == FN_OK) record(MX_VARIANT_GEMM_PAIR, grid, fn::kMgPairThreads, plan.tok, 2);
   return st;
+}
+
+// Bytes of workspace, -1 for sizes or flags that the call refuses.
+int64_t workspace_bytes(const Product& q, bool grouped, bool gather) {
+  Plan plan;
+  if (check_product(q, grouped) != FN_OK) return -1;
+  if (q.M == 0) return 0;
+  if (plan_product(q.M, q.E, q.N, q.K, q.flags, grouped, gather, &plan) != FN_OK) return -1;
+  return plan.workspace();
+}
+
+int run_product(const Product& q, bool grouped, void* stream) {
+  if (int st = check_product(q, grouped)) return st;
+  if (q.M == 0) return FN_OK;
+  Plan plan;
+  if (int st = plan_product(q.M, q.E, q.N, q.K, q.flags, grouped, q.rows != nullptr, &plan))
+    return st;
+  if (int st = check_product_pointers(q, grouped, plan.workspace())) return st;
+  return launch_product(q, grouped, plan, stream);
 }
 
 // ---- silu_mul_quant ---------------------------------------------------------------------
@@ -330,27 +443,36 @@ const char* mx_status_string(int status) {
   }
 }
 
+int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int flags) {
+  Product q = {};
+  q.a_rows = q.M = M, q.E = 1, q.N = q.ldo = N, q.K = K, q.flags = flags;
+  return workspace_bytes(q, false, false);
+}
+
 int mx_gemm(const void* a_q, const void* a_scale, const void* b_q, const void* b_scale, int64_t M,
-            int64_t N, int64_t K, int flags, void* out, int64_t ldo, void* stream) {
+            int64_t N, int64_t K, int flags, void* out, int64_t ldo, void* workspace,
+            void* stream) {
   tl_variant = MX_VARIANT_NONE;
-  const Product q = {a_q, a_scale, b_q, b_scale, nullptr, nullptr, M, 1, M, N, K, ldo, flags, out};
-  if (int st = check_product(q, false)) return st;
-  if (M == 0) return FN_OK;
-  if (int st = check_product_pointers(q, false)) return st;
-  return launch_product(q, false, stream);
+  const Product q = {a_q, a_scale, b_q, b_scale, nullptr, nullptr, M,        1,
+                     M,   N,       K,   ldo,     flags,   out,     workspace};
+  return run_product(q, false, stream);
+}
+
+int64_t mx_grouped_gemm_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K, int flags,
+                                        int gather) {
+  Product q = {};
+  q.a_rows = q.M = R, q.E = E, q.N = q.ldo = N, q.K = K, q.flags = flags;
+  return workspace_bytes(q, true, gather != 0);
 }
 
 int mx_grouped_gemm(const void* a_q, const void* a_scale, int64_t a_rows, const int32_t* rows,
                     const int32_t* offsets, int64_t E, const void* b_q, const void* b_scale,
                     int64_t R, int64_t N, int64_t K, int flags, void* out, int64_t ldo,
-                    void* stream) {
+                    void* workspace, void* stream) {
   tl_variant = MX_VARIANT_NONE;
-  const Product q = {a_q,    a_scale, b_q, b_scale, rows, offsets, a_rows,
-                     E,      R,       N,   K,       ldo,  flags,   out};
-  if (int st = check_product(q, true)) return st;
-  if (R == 0) return FN_OK;
-  if (int st = check_product_pointers(q, true)) return st;
-  return launch_product(q, true, stream);
+  const Product q = {a_q, a_scale, b_q, b_scale, rows,  offsets, a_rows,   E,
+                     R,   N,       K,   ldo,     flags, out,     workspace};
+  return run_product(q, true, stream);
 }
 
 int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H,
@@ -404,7 +526,7 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
     const unsigned threads = (unsigned)round_up((p.nvec + V - 1) / V, 32);
     const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sms * 64);
     const int st = launch(mi.f16 ? act_row<fn::F16>(V) : act_row<fn::Bf16>(V), grid, threads, 0,
-                          stream, 1, p);
+                          stream, 1, tl_pdl != 0, p);
     if (st == FN_OK) record(MX_VARIANT_SILU_ROW, grid, threads, V, 1);
     return st;
   }
@@ -412,7 +534,7 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
       (unsigned)std::min<int64_t>((M * p.nvec + 255) / 256, (int64_t)sms * 64);
   const int st = launch(mi.q == FN_MXFP4 ? act_groups<fn::MODE_MX>(mi.f16)
                                          : act_groups<fn::MODE_G128>(mi.f16),
-                        grid, 256, 0, stream, 1, p);
+                        grid, 256, 0, stream, 1, tl_pdl != 0, p);
   if (st == FN_OK) record(MX_VARIANT_SILU_GROUPS, grid, 256, 1, 1);
   return st;
 }
@@ -453,7 +575,7 @@ int mx_combine(const void* y, int64_t R, const int32_t* pos, const float* weight
   fn::CombineKernel kern = wide ? (f16 ? fn::combine_kernel<fn::F16> : fn::combine_kernel<fn::Bf16>)
                                 : (f16 ? fn::combine_narrow_kernel<fn::F16>
                                        : fn::combine_narrow_kernel<fn::Bf16>);
-  const int st = launch(kern, grid, threads, 0, stream, 1, p);
+  const int st = launch(kern, grid, threads, 0, stream, 1, tl_pdl != 0, p);
   if (st == FN_OK)
     record(wide ? MX_VARIANT_COMBINE : MX_VARIANT_COMBINE_NARROW, grid, threads, 1, 1);
   return st;

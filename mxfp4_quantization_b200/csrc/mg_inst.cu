@@ -1,16 +1,20 @@
-// Instances of the MXFP4 product kernel per token-tile size.
+// Instances of the MXFP4 product kernels.
 #include "mg_kernel.cuh"
+#include "mgp_kernel.cuh"
 
 namespace fn {
 
-MGInstance mg_pick(int tok) {
-  switch (tok) {
-    case 16: return {mg_kernel<16, 1>, 16, 1, MGShape<16, 1>::kSmem};
-    case 64: return {mg_kernel<64, 1>, 64, 1, MGShape<64, 1>::kSmem};
-    case 128: return {mg_kernel<128, 1>, 128, 1, MGShape<128, 1>::kSmem};
-    case 256: return {mg_kernel<256, 2>, 256, 2, MGShape<256, 2>::kSmem};
-    default: return {nullptr, 0, 0, 0};
-  }
+template <int TOK>
+MGInstance instance() {
+  return {mg_kernel<TOK>, TOK, MGShape<TOK>::kSmem, MGShape<TOK>::kPerSm};
 }
+
+MGInstance mg_pick(int tok) {
+  return tok <= 16 ? instance<16>() : tok <= 64 ? instance<64>() : instance<128>();
+}
+
+MGInstance mg_pair() { return {mgp_kernel, kMgPairRows, MGPShape::kSmem, 1}; }
+
+MGArrangeKernel mg_arrange() { return mgp_arrange_kernel; }
 
 }  // namespace fn

@@ -18,7 +18,7 @@ enum : int {
 
 constexpr int kMgFeat = 128;         // output features of a block's tile
 constexpr int kMgStageK = 256;       // elements of a K step (128 bytes of codes a row)
-constexpr int kMgThreads = 288;      // 5 role warps, 4 epilogue warps
+constexpr int kMgThreads = 256;      // 4 role warps, 4 epilogue warps
 constexpr int kMgMaxExperts = 1024;  // the tile table in shared memory
 
 struct MGParams {
@@ -37,7 +37,23 @@ struct MGParams {
   int x_wide, w_wide;       // row-major scale rows are whole aligned 16-byte vectors
   int out_type;
   int out_quads;            // 16-bit output whose rows are whole aligned groups of 4
+  int tok;                  // pair kernel: rows of a tile, a multiple of 16
   int box;                  // rows of a token TMA box (1: gather)
+  int pieces;               // row tiles there can be, over all experts
+  int split;                // blocks (a cluster) that share a tile's K steps
+};
+
+constexpr int kMgPairFeat = 256;     // features of a pair's tile
+constexpr int kMgPairRows = 240;     // rows of a pair's tile, at most
+constexpr int kMgPairThreads = 384;  // 4 role warps, 8 epilogue warps
+
+// What the arranging kernel prepares for the pair kernel, in the workspace.
+struct MGArrange {
+  uint8_t* x_tiles;         // [pieces][2][groups / 4] 512-byte tiles of the rows' scales
+  uint8_t* w_tiles;         // [E][N / 128][groups / 4] tiles of the weights', or nullptr
+  uint4* codes;             // [M, K / 32] gathered codes, or nullptr
+  const uint4* x_codes;
+  int x_swizzled, w_swizzled;
 };
 
 struct MGMaps {
@@ -50,11 +66,15 @@ using MGKernel = void (*)(const MGParams, const MGMaps);
 struct MGInstance {
   MGKernel kernel;
   int tok;       // token rows of a tile
-  int pair;      // blocks that share a tile (cta_group)
   int smem;      // dynamic shared memory without the tile table
+  int per_sm;    // blocks an SM holds
 };
 
-// The instance for a token tile of `tok` rows (16, 64, 128, or 256 over a pair).
+// The single-block instance for a token tile of `tok` rows (16, 64 or 128), and
+// the pair kernel with the kernel that arranges its scales.
+using MGArrangeKernel = void (*)(const MGParams, const MGArrange);
 MGInstance mg_pick(int tok);
+MGInstance mg_pair();
+MGArrangeKernel mg_arrange();
 
 }  // namespace fn

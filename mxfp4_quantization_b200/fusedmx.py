@@ -39,11 +39,13 @@ MX_VARIANT_SILU_GROUPS = 2
 MX_VARIANT_SILU_ROW = 3
 MX_VARIANT_COMBINE = 4
 MX_VARIANT_COMBINE_NARROW = 5
+MX_VARIANT_GEMM_PAIR = 6
 
 OUT_FLAGS = {torch.bfloat16: MX_OUT_BF16, torch.float16: MX_OUT_FP16, torch.float32: MX_OUT_FP32}
 
 # The exported symbols of include/fusedmx.h.
-ABI_SYMBOLS = ("mx_gemm", "mx_grouped_gemm", "mx_silu_mul_quant", "mx_combine",
+ABI_SYMBOLS = ("mx_gemm", "mx_gemm_workspace_bytes", "mx_grouped_gemm",
+               "mx_grouped_gemm_workspace_bytes", "mx_silu_mul_quant", "mx_combine",
                "mx_last_variant", "mx_last_launch", "mx_programmatic_launch",
                "mx_status_string", "mx_version")
 
@@ -60,11 +62,15 @@ def _load():
             f"{LIB_PATH} is not built; run `python -m mxfp4_quantization_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-    lib.mx_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+    lib.mx_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp, vp]
     lib.mx_gemm.restype = i32
+    lib.mx_gemm_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.mx_gemm_workspace_bytes.restype = i64
     lib.mx_grouped_gemm.argtypes = [vp, vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, i32, vp, i64,
-                                    vp]
+                                    vp, vp]
     lib.mx_grouped_gemm.restype = i32
+    lib.mx_grouped_gemm_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32]
+    lib.mx_grouped_gemm_workspace_bytes.restype = i64
     lib.mx_silu_mul_quant.argtypes = [vp, i64, i32, i64, i64, vp, vp, vp, vp, vp]
     lib.mx_silu_mul_quant.restype = i32
     lib.mx_combine.argtypes = [vp, i64, vp, vp, vp, i64, i32, i64, i32, vp, vp]
@@ -89,14 +95,24 @@ _lib = _load()
 
 
 def mx_gemm(a_q, a_scale, b_q, b_scale, M: int, N: int, K: int, flags: int, out, ldo: int,
-            stream: Optional[int]) -> int:
-    return _lib.mx_gemm(a_q, a_scale, b_q, b_scale, M, N, K, flags, out, ldo, stream)
+            workspace, stream: Optional[int]) -> int:
+    return _lib.mx_gemm(a_q, a_scale, b_q, b_scale, M, N, K, flags, out, ldo, workspace, stream)
+
+
+def mx_gemm_workspace_bytes(M: int, N: int, K: int, flags: int) -> int:
+    return _lib.mx_gemm_workspace_bytes(M, N, K, flags)
 
 
 def mx_grouped_gemm(a_q, a_scale, a_rows: int, rows, offsets, E: int, b_q, b_scale, R: int, N: int,
-                    K: int, flags: int, out, ldo: int, stream: Optional[int]) -> int:
+                    K: int, flags: int, out, ldo: int, workspace,
+                    stream: Optional[int]) -> int:
     return _lib.mx_grouped_gemm(a_q, a_scale, a_rows, rows, offsets, E, b_q, b_scale, R, N, K,
-                                flags, out, ldo, stream)
+                                flags, out, ldo, workspace, stream)
+
+
+def mx_grouped_gemm_workspace_bytes(R: int, E: int, N: int, K: int, flags: int,
+                                    gather: int) -> int:
+    return _lib.mx_grouped_gemm_workspace_bytes(R, E, N, K, flags, gather)
 
 
 def mx_silu_mul_quant(x, ldx: int, mode: int, M: int, H: int, num_rows, out_q, out_scale, out_y,
@@ -213,13 +229,27 @@ def _product_out(out, out_dtype, M: int, N: int, device):
     return out, OUT_FLAGS[out.dtype], ldo
 
 
+def _workspace(need: int, given: Optional[torch.Tensor], device):
+    """The call's workspace: `given`, or one from torch's allocator."""
+    if need <= 0:
+        return None
+    if given is None:
+        return torch.empty((need,), dtype=torch.uint8, device=device)
+    if not given.is_cuda or given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if given.numel() * given.element_size() < need:
+        raise ValueError(f"workspace holds fewer than the {need} bytes the call needs")
+    return given
+
+
 def gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: torch.Tensor, *,
-         out: Optional[torch.Tensor] = None,
-         out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+         out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out[m, n] = sum_k a[m, k] b[n, k] of two MXFP4 operands: codes uint8
     [M, K/2] and [N, K/2], scales as quant and rmsnorm_quant return them
     (row-major or in the 32x4x4 tiling).  `out` may have any row stride; its
-    type, else `out_dtype`, is the output type (bfloat16, float16, float32)."""
+    type, else `out_dtype`, is the output type (bfloat16, float16, float32).  The
+    workspace (mx_gemm_workspace_bytes) is allocated with torch unless given."""
     dev = a_q.device
     _tensor(a_q, "a_q", torch.uint8, 2)
     _tensor(b_q, "b_q", torch.uint8, 2, dev)
@@ -229,9 +259,10 @@ def gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: t
     flags = MX_A_SCALE_SWIZZLE if _scale(a_scale, "a_scale", (), M, K, dev) else 0
     flags |= MX_B_SCALE_SWIZZLE if _scale(b_scale, "b_scale", (), N, K, dev) else 0
     out, f, ldo = _product_out(out, out_dtype, M, N, dev)
+    ws = _workspace(mx_gemm_workspace_bytes(M, N, K, flags | f), workspace, dev)
     with torch.cuda.device(dev):
         st = mx_gemm(a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(), M, N,
-                     K, flags | f, out.data_ptr(), ldo, _stream(dev))
+                     K, flags | f, out.data_ptr(), ldo, _ptr(ws), _stream(dev))
     if st != FN_OK:
         raise FusedMXError("mx_gemm", st)
     return out
@@ -240,7 +271,8 @@ def gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: t
 def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
                  b_scale: torch.Tensor, offsets: torch.Tensor, *,
                  rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                 out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                 out_dtype: torch.dtype = torch.bfloat16,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """gemm with one weight per expert: b_q uint8 [E, N, K/2], b_scale
     [E, N, K/32] or [E, bytes of one 32x4x4 tiling]; expert e computes the
     rows offsets[e] <= r < offsets[e+1] (int32 [E+1] on the device) of out
@@ -266,10 +298,12 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     if rows is None and out is not None:
         R = out.shape[0]
     out, f, ldo = _product_out(out, out_dtype, R, N, dev)
+    ws = _workspace(mx_grouped_gemm_workspace_bytes(R, E, N, K, flags | f, int(rows is not None)),
+                    workspace, dev)
     with torch.cuda.device(dev):
         st = mx_grouped_gemm(a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
                              offsets.data_ptr(), E, b_q.data_ptr(), b_scale.data_ptr(), R, N, K,
-                             flags | f, out.data_ptr(), ldo, _stream(dev))
+                             flags | f, out.data_ptr(), ldo, _ptr(ws), _stream(dev))
     if st != FN_OK:
         raise FusedMXError("mx_grouped_gemm", st)
     return out

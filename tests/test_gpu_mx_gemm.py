@@ -92,13 +92,21 @@ def test_extreme_scales(fx):
 
 
 def test_rows_do_not_depend_on_their_neighbours(fx):
-    """A row's bits are the same in a batch of any size (every row tile adds its
-    products in the same order)."""
+    """A row's bits are the same in every batch that adds up its products in the
+    same order: all batches whose tiles are not split along K, and those with
+    the same split."""
     M, N, K = 520, 264, 1312
     aq, as_, bq, bs = operands(M, N, K, 6)
-    whole = fx.gemm(aq, as_, bq, bs, out_dtype=FP)
-    for m in (1, 16, 17, 64, 100, 129, 300):
-        assert torch.equal(fx.gemm(aq[:m], as_[:m], bq, bs, out_dtype=FP), whole[:m])
+    exact, mass = mx_ref.product(mx_ref.values(aq, as_), mx_ref.values(bq, bs))
+    seen = {}
+    for m in (M, 1, 5, 16, 17, 64, 100, 129, 300):
+        out = fx.gemm(aq[:m], as_[:m], bq, bs, out_dtype=FP)
+        mx_ref.check_product(out, exact[:m], mass[:m], K)
+        split = fx.mx_last_launch()[3] if fx.mx_last_variant() == fx.MX_VARIANT_GEMM else 1
+        first = seen.setdefault(split, out)
+        n = min(m, first.shape[0])
+        assert torch.equal(out[:n], first[:n]), (m, split)
+    assert len(seen) > 1
 
 
 def test_replays_streams_and_graphs(fx):

@@ -58,6 +58,8 @@ RAGGED = [
     ([16, 15, 17, 0, 33], 100, 512), ([64, 1, 65, 127], 200, 160), ([128, 0, 129, 3], 257, 1056),
     ([300, 2, 0, 256, 511], 384, 320), ([1] * 40, 128, 64), ([0] * 7 + [90] + [0] * 8, 129, 224),
     ([5] * 65, 72, 2080),
+    # pairs of blocks: row ranges around the tile height of 240 and its even cuts
+    ([240, 241, 0, 480], 256, 256), ([1000, 1, 15, 16, 17], 300, 544), ([239, 700], 513, 96),
 ]
 
 
@@ -85,23 +87,21 @@ def test_rows_without_an_owner_are_left(fx):
     check(fx, [0, 0], 136, 128, FP, first=3, spare=20)
 
 
-def test_offsets_outside_the_contract_stay_in_bounds(fx):
-    """Offsets that run backwards or past the rows: nothing outside out is
-    written, and ranges that are well-formed after clamping are computed."""
-    N, K, R = 128, 128, 40
+@pytest.mark.parametrize("R", [40, 700])
+def test_offsets_outside_the_contract_stay_in_bounds(fx, R):
+    """Offsets that run backwards, overlap or leave the rows: the call ends and
+    nothing outside out is written; the next call is right."""
+    N, K = 128, 128
     aq, as_ = mx_ref.codes(R, K, 3), mx_ref.scales(R, K, 3)
     bq, bs, arg = weights(4, N, K, 4, True)
-    off = torch.tensor([-5, 10, 4, 1000, 20], dtype=torch.int32, device="cuda")
-    g = gpu_util.Guarded((R, N), FP)
-    g.t.fill_(7.0)
-    out = fx.grouped_gemm(aq, as_, bq, arg, off, out=g.t)
-    torch.cuda.synchronize()
-    assert g.intact()
-    a = mx_ref.values(aq, as_)
-    exact, mass = mx_ref.product(a[:4], mx_ref.values(bq[0], bs[0]))
-    mx_ref.check_product(out[:4], exact, mass, K)
-    exact, mass = mx_ref.product(a[10:], mx_ref.values(bq[2], bs[2]))
-    mx_ref.check_product(out[10:], exact, mass, K)
+    for off in ([-5, 10, 4, 1000, 20], [R, 0, R, 0, R], [2 ** 31 - 1, -2 ** 31, R, R, -1],
+                [0, R, 0, R, 0]):
+        off = torch.tensor(off, dtype=torch.int32, device="cuda")
+        g = gpu_util.Guarded((R, N), FP)
+        fx.grouped_gemm(aq, as_, bq, arg, off, out=g.t)
+        torch.cuda.synchronize()
+        assert g.intact()
+    check(fx, [R // 2, 0, R // 4, 3], N, K)
 
 
 def test_many_experts(fx):

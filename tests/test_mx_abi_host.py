@@ -69,10 +69,11 @@ def test_status_strings_and_settings(fx):
 
 
 def gemm(fx, **kw):
-    a = dict(aq=at(1), as_=at(2), bq=at(3), bs=at(4), M=8, N=72, K=96, flags=0, out=at(5), ldo=72)
+    a = dict(aq=at(1), as_=at(2), bq=at(3), bs=at(4), M=8, N=72, K=96, flags=0, out=at(5), ldo=72,
+             ws=at(8))
     a.update(kw)
     return fx.mx_gemm(a["aq"], a["as_"], a["bq"], a["bs"], a["M"], a["N"], a["K"], a["flags"],
-                      a["out"], a["ldo"], None)
+                      a["out"], a["ldo"], a["ws"], None)
 
 
 GEMM_RULES = [
@@ -118,10 +119,34 @@ def test_gemm_accepts(fx, kw):
 
 def grouped(fx, **kw):
     a = dict(aq=at(1), as_=at(2), a_rows=8, rows=None, off=at(6), E=3, bq=at(3), bs=at(4), R=8,
-             N=72, K=96, flags=0, out=at(5), ldo=72)
+             N=72, K=96, flags=0, out=at(5), ldo=72, ws=at(8))
     a.update(kw)
     return fx.mx_grouped_gemm(a["aq"], a["as_"], a["a_rows"], a["rows"], a["off"], a["E"], a["bq"],
-                              a["bs"], a["R"], a["N"], a["K"], a["flags"], a["out"], a["ldo"], None)
+                              a["bs"], a["R"], a["N"], a["K"], a["flags"], a["out"], a["ldo"],
+                              a["ws"], None)
+
+
+def test_workspace_rules(fx):
+    """A call of many rows takes a workspace: it has to be there, aligned and
+    apart from every tensor of the call; a call of few rows needs none."""
+    M, N, K = 500, 512, 1024
+    need = fx.mx_gemm_workspace_bytes(M, N, K, 0)
+    assert need > 0 and need % 16 == 0
+    assert 0 < fx.mx_gemm_workspace_bytes(M, N, K, 0x20) < need  # tiled weights stay where they are
+    assert fx.mx_gemm_workspace_bytes(8, N, K, 0) == 0 and gemm(fx, M=8, ws=None) in (0, CUDA)
+    assert fx.mx_gemm_workspace_bytes(0, N, K, 0) == 0
+    for bad in ((-1, N, K, 0), (M, 0, K, 0), (M, N, 48, 0), (M, N, K, 3), (M, N, 1 << 25, 0)):
+        assert fx.mx_gemm_workspace_bytes(*bad) == -1
+    g = fx.mx_grouped_gemm_workspace_bytes(M, 2, N, K, 0x20, 0)
+    assert fx.mx_grouped_gemm_workspace_bytes(M, 2, N, K, 0x20, 1) == g + M * K // 2
+    assert fx.mx_grouped_gemm_workspace_bytes(M, 2, N, K, 0x10, 0) == -1
+    big = dict(M=M, N=N, K=K, ldo=N)
+    for kw, want in ((dict(ws=None), E), (dict(ws=at(8, 8)), A), (dict(ws=at(1)), E),
+                     (dict(ws=at(5, 16)), E), (dict(ws=at(4) - need + 16), E),
+                     (dict(ws=at(3, N * K // 2 - 16)), E)):
+        assert gemm(fx, **big, **kw) == want, kw
+    assert grouped(fx, R=M, a_rows=M, E=2, N=N, K=K, ldo=N, ws=at(6, 0)) == E
+    assert grouped(fx, R=M, a_rows=5, rows=at(7), E=2, N=N, K=K, ldo=N, ws=at(7, 1984)) == E
 
 
 GROUPED_RULES = [
@@ -237,6 +262,7 @@ def test_combine_accepts(fx, kw):
 def test_every_device_wait_is_bounded():
     """The kernels spin only through the bounded waits."""
     csrc = os.path.join(ROOT, "mxfp4_quantization_b200", "csrc")
-    for name in ("tc_device.cuh", "mg_kernel.cuh", "act_kernel.cuh", "combine_kernel.cuh"):
+    for name in ("tc_device.cuh", "mg_kernel.cuh", "mgp_kernel.cuh", "mg_common.cuh",
+                 "act_kernel.cuh", "combine_kernel.cuh"):
         src = open(os.path.join(csrc, name)).read()
         assert not re.search(r"while\s*\(\s*!\s*mbar|while\s*\(\s*(true|1)\s*\)|for\s*\(\s*;\s*;", src)
