@@ -52,6 +52,9 @@ extern "C" {
 
 #define MX_MAX_EXPERTS 1024
 #define MX_MAX_TOP 32
+/* Products of at most this many rows (an average of that many per expert) need
+ * no workspace. */
+#define MX_SMALL_ROWS 128
 
 /*
  * Product of two MXFP4 operands (a linear layer on quantized rows):

@@ -246,7 +246,7 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
   const int64_t each = grouped ? ceil_div(M, E) : M;
   const int64_t more = grouped ? std::min(E, M) : 0;  // a partly filled tile an expert
   const int64_t groups = K / 32, kts = ceil_div(groups, 4);
-  p.pair = each > 128;
+  p.pair = each > MX_SMALL_ROWS;
   if (p.pair) {
     p.feat = ceil_div(N, fn::kMgPairFeat);
     p.tok = fn::kMgPairRows;

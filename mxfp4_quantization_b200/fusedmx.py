@@ -32,6 +32,7 @@ MX_A_SCALE_SWIZZLE = 0x10
 MX_B_SCALE_SWIZZLE = 0x20
 MX_MAX_EXPERTS = 1024
 MX_MAX_TOP = 32
+MX_SMALL_ROWS = 128
 
 MX_VARIANT_NONE = 0
 MX_VARIANT_GEMM = 1
@@ -169,12 +170,26 @@ class programmatic_launch:
 SiluMulQuantOutput = namedtuple("SiluMulQuantOutput", "q scale y")
 
 
+# A decode step makes these calls every few microseconds, so the checks below read
+# each attribute of a tensor once and build nothing they do not need.
+
+_U8, _I32 = torch.uint8, torch.int32
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(func, device, *args) -> int:
+    """func(*args, stream) on the current stream of `device`, with that device
+    current."""
+    i = device.index
+    if i == _current_device():
+        return func(*args, _raw_stream(i))
+    with torch.cuda.device(device):
+        return func(*args, _raw_stream(i))
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
-
-
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _round_up(x: int, m: int) -> int:
@@ -185,7 +200,7 @@ def _tensor(t: torch.Tensor, name: str, dtype, dim=None, device=None) -> torch.T
     """A contiguous CUDA tensor of `dtype` on the call's device."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
@@ -196,37 +211,50 @@ def _tensor(t: torch.Tensor, name: str, dtype, dim=None, device=None) -> torch.T
     return t
 
 
-def _scale(t: torch.Tensor, name: str, lead: tuple, rows: int, K: int, device) -> bool:
-    """Checks E8M0 scales of [*lead, rows, K/32] values; True if they are in
-    the 32x4x4 tiling (flat per leading index)."""
-    if t.dtype != torch.uint8 and t.dtype != torch.float8_e8m0fnu:
+def _scale(t: torch.Tensor, name: str, lead: int, rows: int, G: int, device) -> bool:
+    """Checks E8M0 scales of `rows` rows of G groups (per expert, if lead is the
+    number of experts and not 0); True if they are in the 32x4x4 tiling (flat
+    per expert)."""
+    if t.dtype is not _U8 and t.dtype is not torch.float8_e8m0fnu:
         raise TypeError(f"{name} must be uint8 (E8M0 bytes), got {t.dtype}")
-    _tensor(t, name, t.dtype, None, device)
-    n = _round_up(rows, 128) * _round_up(K // 32, 4)
-    if tuple(t.shape) == (*lead, rows, K // 32):
-        return False
-    if tuple(t.shape) == (*lead, n):
+    if not t.is_cuda or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    shape = t.shape
+    if lead:
+        if shape[0] == lead:
+            shape = shape[1:]
+        else:
+            shape = ()
+    if len(shape) == 2:
+        if shape[0] == rows and shape[1] == G:
+            return False
+    elif len(shape) == 1 and shape[0] == _round_up(rows, 128) * _round_up(G, 4):
         return True
-    raise ValueError(f"{name} has shape {tuple(t.shape)}: expected {(*lead, rows, K // 32)}, or "
-                     f"{(*lead, n)} in the 32x4x4 tiling")
+    first = f"{lead}, " if lead else ""
+    raise ValueError(f"{name} has shape {tuple(t.shape)}: expected ({first}{rows}, {G}), or "
+                     f"({first}{_round_up(rows, 128) * _round_up(G, 4)}) in the 32x4x4 tiling")
 
 
 def _product_out(out, out_dtype, M: int, N: int, device):
     """The output tensor, its flag and its row stride."""
     if out is None:
-        if out_dtype not in OUT_FLAGS:
+        flag = OUT_FLAGS.get(out_dtype)
+        if flag is None:
             raise TypeError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
+        return torch.empty((M, N), dtype=out_dtype, device=device), flag, N
     if not out.is_cuda or out.device != device:
         raise ValueError(f"out must be on {device}")
-    if out.dtype not in OUT_FLAGS:
+    flag = OUT_FLAGS.get(out.dtype)
+    if flag is None:
         raise TypeError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
-    if tuple(out.shape) != (M, N):
+    if out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, N)}")
-    ldo = out.stride(0) if M > 1 else max(N, out.stride(0))
-    if (N > 1 and out.stride(1) != 1) or ldo < N:
+    ldo, step = out.stride()
+    if M <= 1:
+        ldo = max(N, ldo)
+    if (N > 1 and step != 1) or ldo < N:
         raise ValueError("out needs a contiguous last dim and rows that do not overlap")
-    return out, OUT_FLAGS[out.dtype], ldo
+    return out, flag, ldo
 
 
 def _workspace(need: int, given: Optional[torch.Tensor], device):
@@ -234,7 +262,7 @@ def _workspace(need: int, given: Optional[torch.Tensor], device):
     if need <= 0:
         return None
     if given is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device)
+        return torch.empty((need,), dtype=_U8, device=device)
     if not given.is_cuda or given.device != device or not given.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if given.numel() * given.element_size() < need:
@@ -251,18 +279,22 @@ def gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: t
     type, else `out_dtype`, is the output type (bfloat16, float16, float32).  The
     workspace (mx_gemm_workspace_bytes) is allocated with torch unless given."""
     dev = a_q.device
-    _tensor(a_q, "a_q", torch.uint8, 2)
-    _tensor(b_q, "b_q", torch.uint8, 2, dev)
-    M, N, K = a_q.shape[0], b_q.shape[0], 2 * a_q.shape[1]
-    if b_q.shape[1] != a_q.shape[1]:
-        raise ValueError(f"a_q rows have {K} codes, b_q rows {2 * b_q.shape[1]}")
-    flags = MX_A_SCALE_SWIZZLE if _scale(a_scale, "a_scale", (), M, K, dev) else 0
-    flags |= MX_B_SCALE_SWIZZLE if _scale(b_scale, "b_scale", (), N, K, dev) else 0
+    _tensor(a_q, "a_q", _U8, 2)
+    _tensor(b_q, "b_q", _U8, 2, dev)
+    M, half = a_q.shape
+    N, other = b_q.shape
+    if half != other:
+        raise ValueError(f"a_q rows have {2 * half} codes, b_q rows {2 * other}")
+    flags = MX_A_SCALE_SWIZZLE if _scale(a_scale, "a_scale", 0, M, half // 16, dev) else 0
+    if _scale(b_scale, "b_scale", 0, N, half // 16, dev):
+        flags |= MX_B_SCALE_SWIZZLE
     out, f, ldo = _product_out(out, out_dtype, M, N, dev)
-    ws = _workspace(mx_gemm_workspace_bytes(M, N, K, flags | f), workspace, dev)
-    with torch.cuda.device(dev):
-        st = mx_gemm(a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(), M, N,
-                     K, flags | f, out.data_ptr(), ldo, _ptr(ws), _stream(dev))
+    flags |= f
+    ws = None
+    if M > MX_SMALL_ROWS:
+        ws = _workspace(mx_gemm_workspace_bytes(M, N, 2 * half, flags), workspace, dev)
+    st = _call(_lib.mx_gemm, dev, a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(),
+               b_scale.data_ptr(), M, N, 2 * half, flags, out.data_ptr(), ldo, _ptr(ws))
     if st != FN_OK:
         raise FusedMXError("mx_gemm", st)
     return out
@@ -277,33 +309,34 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     [E, N, K/32] or [E, bytes of one 32x4x4 tiling]; expert e computes the
     rows offsets[e] <= r < offsets[e+1] (int32 [E+1] on the device) of out
     from the rows `rows[r]` (int32 [R]) of a, or from row r itself.  out has
-    as many rows as `rows`, else as a_q; rows that no expert owns keep what
-    they held (a new out is not filled)."""
+    as many rows as `rows`, else as a_q (an out that is given may have fewer);
+    rows that no expert owns keep what they held (a new out is not filled)."""
     dev = a_q.device
-    _tensor(a_q, "a_q", torch.uint8, 2)
-    _tensor(b_q, "b_q", torch.uint8, 3, dev)
-    _tensor(offsets, "offsets", torch.int32, 1, dev)
-    a_rows, K = a_q.shape[0], 2 * a_q.shape[1]
-    E, N = b_q.shape[0], b_q.shape[1]
-    if b_q.shape[2] != a_q.shape[1]:
-        raise ValueError(f"a_q rows have {K} codes, b_q rows {2 * b_q.shape[2]}")
+    _tensor(a_q, "a_q", _U8, 2)
+    _tensor(b_q, "b_q", _U8, 3, dev)
+    _tensor(offsets, "offsets", _I32, 1, dev)
+    a_rows, half = a_q.shape
+    E, N, other = b_q.shape
+    if half != other:
+        raise ValueError(f"a_q rows have {2 * half} codes, b_q rows {2 * other}")
     if offsets.shape[0] != E + 1:
         raise ValueError(f"offsets has {offsets.shape[0]} entries, expected {E + 1}")
-    if _scale(a_scale, "a_scale", (), a_rows, K, dev):
+    if _scale(a_scale, "a_scale", 0, a_rows, half // 16, dev):
         raise ValueError("a_scale must be row-major [rows, K/32] for ragged row ranges")
-    flags = MX_B_SCALE_SWIZZLE if _scale(b_scale, "b_scale", (E,), N, K, dev) else 0
+    flags = MX_B_SCALE_SWIZZLE if _scale(b_scale, "b_scale", E, N, half // 16, dev) else 0
     if rows is not None:
-        _tensor(rows, "rows", torch.int32, 1, dev)
-    R = a_rows if rows is None else rows.shape[0]
-    if rows is None and out is not None:
-        R = out.shape[0]
+        R = _tensor(rows, "rows", _I32, 1, dev).shape[0]
+    else:
+        R = a_rows if out is None else min(a_rows, out.shape[0])
     out, f, ldo = _product_out(out, out_dtype, R, N, dev)
-    ws = _workspace(mx_grouped_gemm_workspace_bytes(R, E, N, K, flags | f, int(rows is not None)),
-                    workspace, dev)
-    with torch.cuda.device(dev):
-        st = mx_grouped_gemm(a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
-                             offsets.data_ptr(), E, b_q.data_ptr(), b_scale.data_ptr(), R, N, K,
-                             flags | f, out.data_ptr(), ldo, _ptr(ws), _stream(dev))
+    flags |= f
+    ws = None
+    if R > MX_SMALL_ROWS * E:
+        ws = _workspace(mx_grouped_gemm_workspace_bytes(R, E, N, 2 * half, flags,
+                                                        int(rows is not None)), workspace, dev)
+    st = _call(_lib.mx_grouped_gemm, dev, a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
+               offsets.data_ptr(), E, b_q.data_ptr(), b_scale.data_ptr(), R, N, 2 * half, flags,
+               out.data_ptr(), ldo, _ptr(ws))
     if st != FN_OK:
         raise FusedMXError("mx_grouped_gemm", st)
     return out
@@ -342,19 +375,21 @@ def silu_mul_quant(x: torch.Tensor, mode: Union[int, str], *,
     dev = x.device
     if num_rows is not None and _tensor(num_rows, "num_rows", torch.int32, None, dev).numel() != 1:
         raise ValueError("num_rows must hold one value")
-    if out_q is None or out_scale is None:
-        q, s = alloc_outputs(m, M, H, dev)
-        out_q = q if out_q is None else out_q
-        out_scale = s if out_scale is None else out_scale
-    _check_quant(out_q, out_scale, m, M, H, dev)
+    if out_q is None and out_scale is None:
+        out_q, out_scale = alloc_outputs(m, M, H, dev)
+    else:
+        if out_q is None or out_scale is None:
+            q, s = alloc_outputs(m, M, H, dev)
+            out_q = q if out_q is None else out_q
+            out_scale = s if out_scale is None else out_scale
+        _check_quant(out_q, out_scale, m, M, H, dev)
     if out_y is None and emit_y:
         out_y = torch.empty((M, H), dtype=x.dtype, device=dev)
     elif out_y is not None:
         if _tensor(out_y, "out_y", x.dtype, None, dev).numel() != M * H:
             raise ValueError(f"out_y must hold {M} x {H} values")
-    with torch.cuda.device(dev):
-        st = mx_silu_mul_quant(x.data_ptr(), ldx, m, M, H, _ptr(num_rows), out_q.data_ptr(),
-                               out_scale.data_ptr(), _ptr(out_y), _stream(dev))
+    st = _call(_lib.mx_silu_mul_quant, dev, x.data_ptr(), ldx, m, M, H, _ptr(num_rows),
+               out_q.data_ptr(), out_scale.data_ptr(), _ptr(out_y))
     if st != FN_OK:
         raise FusedMXError("mx_silu_mul_quant", st)
     return SiluMulQuantOutput(out_q, out_scale, out_y)
@@ -384,24 +419,25 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, *,
     """out[t] = base[t] + sum_j weight[t, j] y[pos[t, j]]: y bf16 (or float16)
     [R, N], pos int32 [T, k] (positions outside [0, R) are skipped), weight
     fp32 [T, k], base and out of y's type [T, N] (out may be base)."""
-    if y.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"y must be bfloat16 or float16, got {y.dtype}")
-    _tensor(y, "y", y.dtype, 2)
+    dt = y.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"y must be bfloat16 or float16, got {dt}")
+    _tensor(y, "y", dt, 2)
     dev = y.device
-    _tensor(pos, "pos", torch.int32, 2, dev)
+    _tensor(pos, "pos", _I32, 2, dev)
     _tensor(weight, "weight", torch.float32, 2, dev)
+    R, N = y.shape
+    T, k = pos.shape
     if weight.shape != pos.shape:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, pos {tuple(pos.shape)}")
-    (R, N), (T, k) = y.shape, pos.shape
+    if base is not None and _tensor(base, "base", dt, 2, dev).shape != (T, N):
+        raise ValueError(f"base has shape {tuple(base.shape)}, expected {(T, N)}")
     if out is None:
-        out = torch.empty((T, N), dtype=y.dtype, device=dev)
-    for t, name in ((base, "base"), (out, "out")):
-        if t is not None and tuple(_tensor(t, name, y.dtype, 2, dev).shape) != (T, N):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, N)}")
-    flags = FN_IO_FP16 if y.dtype == torch.float16 else 0
-    with torch.cuda.device(dev):
-        st = mx_combine(y.data_ptr(), R, pos.data_ptr(), weight.data_ptr(), _ptr(base), T, k, N,
-                        flags, out.data_ptr(), _stream(dev))
+        out = torch.empty((T, N), dtype=dt, device=dev)
+    elif _tensor(out, "out", dt, 2, dev).shape != (T, N):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, N)}")
+    st = _call(_lib.mx_combine, dev, y.data_ptr(), R, pos.data_ptr(), weight.data_ptr(),
+               _ptr(base), T, k, N, FN_IO_FP16 if dt is torch.float16 else 0, out.data_ptr())
     if st != FN_OK:
         raise FusedMXError("mx_combine", st)
     return out
