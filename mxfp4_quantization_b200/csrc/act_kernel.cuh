@@ -60,47 +60,142 @@ __device__ __noinline__ uint32_t silu_mul_fp64(float g, float u) {
   return IO::pack(f, 0.f) & 0xFFFFu;
 }
 
+// The same for the elements that fp32 leaves open, in about 50 instructions (the
+// form above takes 300): e^-g as 2^n 2^f, the Taylor polynomial of e^(f ln 2) to
+// degree 11 (|f ln 2| <= 0.347: 2^-47), the reciprocal of 1 + e^-g by two
+// Newton-Raphson steps on the fp32 approximation; 2^-45 in all.  Where the result
+// is that near a midpoint (twice over), outside the type's normal range, or g < -87,
+// the form above decides.
+template <class IO>
+__device__ __forceinline__ uint32_t silu_mul_mid(float g, float u) {
+  const double gd = g, t = gd * -1.4426950408889634074;
+  const double n = rint(t), x = (t - n) * 0.69314718055994530942;
+  double e = 1.0 / 39916800;
+  e = fma(e, x, 1.0 / 3628800);
+  e = fma(e, x, 1.0 / 362880);
+  e = fma(e, x, 1.0 / 40320);
+  e = fma(e, x, 1.0 / 5040);
+  e = fma(e, x, 1.0 / 720);
+  e = fma(e, x, 1.0 / 120);
+  e = fma(e, x, 1.0 / 24);
+  e = fma(e, x, 1.0 / 6);
+  e = fma(e, x, 0.5);
+  e = fma(e, x, 1.0);
+  e = fma(e, x, 1.0);
+  const int ni = g >= -87.f && g <= 700.f ? (int)n : 0;
+  const double d = 1.0 + __hiloint2double(__double2hiint(e) + (ni << 20), __double2loint(e));
+  float rf;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rf) : "f"((float)d));
+  double r = rf;
+  r = fma(fma(-d, r, 1.0), r, r);
+  r = fma(fma(-d, r, 1.0), r, r);
+  const double v = gd * (double)u * r;
+  constexpr int kCut = IO::kF16 ? 42 : 45;  // mantissa bits beyond the 16-bit type's
+  const uint64_t rest = (uint64_t)__double_as_longlong(v) & ((1ull << kCut) - 1);
+  const int64_t off = (int64_t)rest - (int64_t)(1ull << (kCut - 1));
+  const double mag = fabs(v);
+  const bool sure = g >= -87.f && g <= 700.f && (off > 1 << 10 || off < -(1 << 10)) &&
+                    mag >= (IO::kF16 ? 0x1p-14 : 0x1p-100) && mag < (IO::kF16 ? 65504.0 : 0x1p127);
+  if (!sure) return silu_mul_fp64<IO>(g, u);
+  // cut to fp32 with the last bit set: on the same side of every midpoint
+  const float f = __uint_as_float(__float_as_uint(__double2float_rz(v)) | 1u);
+  return IO::pack(f, 0.f) & 0xFFFFu;
+}
+
 // fp32 value of g u / (1 + e^-g), relative error below kSiluErr where it is used
 // (g >= -87, |result| >= 2^-100).  e^-g = 2^t with t = -g log2(e) in two parts:
 // the rounded product and its remainder, which scales the result by 1 + t_lo ln 2.
 // Errors, in units of 2^-24: ex2.approx 4 (2^-22), the remainder's terms 1, their
 // product 1, the sum 1 + e^-g 1 (and it passes on at most the 6 before), the
-// approximate reciprocal 2, two products 2: 12 in all, below 2^-20.4.
+// approximate reciprocal 2, two products 2: 12 in all, below 2^-20.4.  (The .ftz
+// forms: an e^-g below 2^-126 adds nothing to 1, and 1 + e^-g stays below 2^126,
+// so neither result that matters is subnormal.)
 constexpr float kSiluErr = 0x1p-20f;
 
-__device__ __forceinline__ float silu_mul_fp32(float g, float u) {
+__device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   constexpr float kLog2e = 1.44269504088896340736f;
   constexpr float kLog2eLo = 1.92596299112661746887e-8f;  // log2(e) - kLog2e
-  const float t = -g * kLog2e;
-  const float lo = fmaf(-g, kLog2eLo, fmaf(-g, kLog2e, -t));
-  float e, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
-  e = fmaf(e, lo * 0.693147180559945309417f, e);
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return (g * r) * u;  // g u alone can overflow where the result does not
+  constexpr float kLn2 = 0.693147180559945309417f;
+  const float2 c = make_float2(-kLog2e, -kLog2e);
+  const float2 t = mul_f32x2(g, c);
+  float2 lo = fma_f32x2(g, c, make_float2(-t.x, -t.y));
+  lo = fma_f32x2(g, make_float2(-kLog2eLo, -kLog2eLo), lo);
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = fma_f32x2(e, mul_f32x2(lo, make_float2(kLn2, kLn2)), e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
+  return mul_f32x2(mul_f32x2(g, r), u);  // g u alone can overflow where the result does not
 }
 
-// y of one element pair (gate word, up word).
+// The smallest value, NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t half_of(const uint4& v, int i) {
+  return word(v, i >> 1) >> (16 * (i & 1)) & 0xFFFFu;
+}
+
+// Recomputes the elements of `mask`: every lane its own next one, so lanes that
+// missed different elements share a pass.
 template <class IO>
-__device__ __forceinline__ uint32_t silu_mul_pair(uint32_t gw, uint32_t uw) {
-  const float g0 = IO::lo(gw), g1 = IO::hi(gw), u0 = IO::lo(uw), u1 = IO::hi(uw);
-  const float v0 = silu_mul_fp32(g0, u0), v1 = silu_mul_fp32(g1, u1);
-  // the two ends of the interval that holds the real value round to one
-  // 16-bit value unless a midpoint lies between them
-  const uint32_t a = IO::pack(v0 * (1.f - kSiluErr), v1 * (1.f - kSiluErr));
-  uint32_t y = IO::pack(v0 * (1.f + kSiluErr), v1 * (1.f + kSiluErr));
-  // outside the interval's range (a zero is exact, or far below every 16-bit value)
-  const bool far0 = !(g0 >= -87.f) || !(fabsf(v0) >= 0x1p-100f || v0 == 0.f),
-             far1 = !(g1 >= -87.f) || !(fabsf(v1) >= 0x1p-100f || v1 == 0.f);
-  if (((a ^ y) & 0xFFFFu) || far0) y = (y & 0xFFFF0000u) | silu_mul_fp64<IO>(g0, u0);
-  if (((a ^ y) >> 16) || far1) y = (y & 0xFFFFu) | silu_mul_fp64<IO>(g1, u1) << 16;
+__device__ __noinline__ uint4 silu_mul_redo(uint4 g, uint4 u, uint4 y, uint32_t mask) {
+  while (mask) {
+    const int i = __ffs(mask) - 1, w = i >> 1, sh = 16 * (i & 1);
+    mask &= mask - 1;
+    const uint32_t r = silu_mul_mid<IO>(IO::lo(half_of(g, i)), IO::lo(half_of(u, i)));
+    set_word(y, w, (word(y, w) & ~(0xFFFFu << sh)) | r << sh);
+  }
   return y;
 }
 
+// y of 8 elements.  The two ends of the interval that holds the real value
+// round to one 16-bit value unless a midpoint lies between them; one test
+// covers all 8 (bf16: 9 % of warps fail it somewhere, binary16: half).
 template <class IO>
-__device__ __forceinline__ uint4 silu_mul_vec(const uint4& g, const uint4& u) {
-  return make_uint4(silu_mul_pair<IO>(g.x, u.x), silu_mul_pair<IO>(g.y, u.y),
-                    silu_mul_pair<IO>(g.z, u.z), silu_mul_pair<IO>(g.w, u.w));
+__device__ __forceinline__ uint4 silu_mul_vec(const uint4& gv, const uint4& uv) {
+  uint32_t a[4], y[4], differ = 0;
+  float2 v[4];
+  float vmin = 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 g = make_float2(IO::lo(word(gv, i)), IO::hi(word(gv, i)));
+    const float2 u = make_float2(IO::lo(word(uv, i)), IO::hi(word(uv, i)));
+    v[i] = silu_mul_fp32(g, u);
+    const float2 l = mul_f32x2(v[i], make_float2(1.f - kSiluErr, 1.f - kSiluErr));
+    const float2 h = mul_f32x2(v[i], make_float2(1.f + kSiluErr, 1.f + kSiluErr));
+    a[i] = IO::pack(l.x, l.y);
+    y[i] = IO::pack(h.x, h.y);
+    differ |= a[i] ^ y[i];
+    vmin = min_nan(vmin, fabsf(v[i].x), fabsf(v[i].y));
+  }
+  uint4 out = make_uint4(y[0], y[1], y[2], y[3]);
+  // (g below -87.3, where 1 / (1 + e^-g) leaves the normal range, gives 0 here)
+  const bool far = !(vmin >= 0x1p-100f);
+  if (differ != 0 || far) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = a[i] ^ y[i];
+      if (x & 0xFFFFu) mask |= 1u << (2 * i);
+      if (x >> 16) mask |= 2u << (2 * i);
+    }
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g0 = IO::lo(word(gv, i)), g1 = IO::hi(word(gv, i));
+        // outside the interval's range (a zero is exact, or far below every 16-bit value)
+        if (!(g0 >= -87.f) || !(fabsf(v[i].x) >= 0x1p-100f || v[i].x == 0.f)) mask |= 1u << (2 * i);
+        if (!(g1 >= -87.f) || !(fabsf(v[i].y) >= 0x1p-100f || v[i].y == 0.f)) mask |= 2u << (2 * i);
+      }
+    }
+    if (mask) out = silu_mul_redo<IO>(gv, uv, out, mask);
+  }
+  return out;
 }
 
 __device__ __forceinline__ int64_t act_rows(const ActParams& p) {
@@ -109,50 +204,84 @@ __device__ __forceinline__ int64_t act_rows(const ActParams& p) {
   return n < 0 ? 0 : n < p.M ? n : p.M;
 }
 
-// Group modes (MXFP4, FP8 per 128): a thread per 8-element vector of the rows
-// laid end to end; groups are 4 or 16 neighbouring lanes.
-template <int MODE, class IO>
-__global__ void __launch_bounds__(256) act_groups_kernel(const ActParams p) {
+// Group modes (MXFP4, FP8 per 128): the rows laid end to end, kActVecs 8-element
+// vectors a thread with all their loads first (two where there is work for
+// it, one for decode-sized calls); groups are 4 or 16 neighbouring lanes.
+// Bound by instructions, 33 an element: two special-function operations, ten packed
+// fp32, the interval test, the quantization.  32768 x 2048: MXFP4 from bf16 78 us
+// (3.9 TB/s), FP8 per 128 89 us; from binary16, whose midpoints lie eight times as
+// close, 99 and 110 us.  With four blocks an SM instead of six 85 us, with
+// four vectors a thread 75 and 89 (binary16 100 and 116).
+template <int MODE, class IO, int kActVecs>
+__global__ void __launch_bounds__(256, 6) act_groups_kernel(const ActParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t total = act_rows(p) * p.nvec;
-  for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x; i0 < total;
-       i0 += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool ok = i < total;
-    const int64_t row = ok ? i / p.nvec : 0;
-    const int v = ok ? (int)(i - row * p.nvec) : 0;
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (ok) {
-      const uint4* src = p.x + row * p.ldv + v;
-      y = silu_mul_vec<IO>(ld_stream_nc(src), ld_stream_nc(src + p.nvec));
-      if (p.out_y) st_stream(p.out_y + row * p.nvec + v, y);
+  const int64_t rows = act_rows(p), total = rows * p.nvec;
+  for (int64_t i0 = (int64_t)blockIdx.x * (256 * kActVecs); i0 < total;
+       i0 += (int64_t)gridDim.x * (256 * kActVecs)) {
+    // one 64-bit division a block; a vector is then at most 511 past (r0, v0)
+    const int64_t r0 = i0 / p.nvec;
+    const int v0 = (int)(i0 - r0 * p.nvec);
+    int64_t row[kActVecs];
+    int v[kActVecs];
+    bool ok[kActVecs];
+    uint4 g[kActVecs], u[kActVecs];
+#pragma unroll
+    for (int k = 0; k < kActVecs; ++k) {
+      const unsigned at = (unsigned)(v0 + k * 256 + (int)threadIdx.x);
+      const unsigned down = p.nvec >= 256 * kActVecs ? (at >= (unsigned)p.nvec ? 1u : 0u)
+                                                     : at / (unsigned)p.nvec;
+      row[k] = r0 + down;
+      v[k] = (int)(at - down * (unsigned)p.nvec);
+      ok[k] = row[k] < rows;
+      if (!ok[k]) row[k] = 0, v[k] = 0;
+      const uint4* src = p.x + row[k] * p.ldv + v[k];
+      g[k] = ld_stream_nc(src);
+      u[k] = ld_stream_nc(src + p.nvec);
     }
-    quant_store<MODE, IO>(y, ok, lane, row, v, p.nvec * 8, Fp8Scale{1.f, 1.f, 0.f, false},
-                          p.out_q, p.out_scale, p.scale_layout, p.scale_ld);
+#pragma unroll
+    for (int k = 0; k < kActVecs; ++k) {
+      const uint4 y = silu_mul_vec<IO>(g[k], u[k]);
+      if (p.out_y && ok[k]) st_stream(p.out_y + row[k] * p.nvec + v[k], y);
+      quant_store<MODE, IO>(y, ok[k], lane, row[k], v[k], p.nvec * 8,
+                            Fp8Scale{1.f, 1.f, 0.f, false}, p.out_q, p.out_scale, p.scale_layout,
+                            p.scale_ld);
+    }
   }
 }
 
 // Per-token mode: a block per row, the row in registers (V vectors a thread)
-// between the maximum and the codes.
+// between the maximum and the codes.  bf16, 67 M elements: 92 us at H = 2048, 69 us
+// (4.8 TB/s) at 8192, 77 us at 16384; the blocks an SM are held to were
+// measured (16384: 87 us at two, 144 us at one).
 template <int V, class IO>
-__global__ void __launch_bounds__(1024) act_row_kernel(const ActParams p) {
+__global__ void __launch_bounds__(256, V == 1 ? 8 : V == 2 ? 6 : V == 4 ? 4 : V == 8 ? 3 : 1) act_row_kernel(const ActParams p) {
   pdl_enter();
-  __shared__ float red[32];
+  __shared__ float red[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
   const int64_t rows = act_rows(p);
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    constexpr int B = V < 4 ? V : 4;  // vectors whose loads are in flight together
     uint4 y[V];
     float am = 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
-      y[k] = make_uint4(0, 0, 0, 0);
-      if (v < p.nvec) {
-        const uint4* src = p.x + row * p.ldv + v;
-        y[k] = silu_mul_vec<IO>(ld_stream_nc(src), ld_stream_nc(src + p.nvec));
-        if (p.out_y) st_stream(p.out_y + row * p.nvec + v, y[k]);
-        am = fmaxf(am, vec_absmax<IO>(y[k]));
+    for (int k0 = 0; k0 < V; k0 += B) {
+      uint4 g[B], u[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const int v = threadIdx.x + (k0 + k) * blockDim.x;
+        const uint4* src = p.x + row * p.ldv + (v < p.nvec ? v : 0);
+        g[k] = ld_stream_nc(src);
+        u[k] = ld_stream_nc(src + p.nvec);
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const int v = threadIdx.x + (k0 + k) * blockDim.x;
+        y[k0 + k] = silu_mul_vec<IO>(g[k], u[k]);
+        if (v < p.nvec) {
+          if (p.out_y) st_stream(p.out_y + row * p.nvec + v, y[k0 + k]);
+          am = fmaxf(am, vec_absmax<IO>(y[k0 + k]));
+        }
       }
     }
     am = warp_max(am);

@@ -403,15 +403,20 @@ int parse_mode(int mode, ModeInfo* mi) {
 }
 
 template <int MODE>
-fn::ActKernel act_groups(bool f16) {
-  return f16 ? fn::act_groups_kernel<MODE, fn::F16> : fn::act_groups_kernel<MODE, fn::Bf16>;
+fn::ActKernel act_groups(bool f16, int vecs) {
+  return vecs == 1 ? (f16 ? fn::act_groups_kernel<MODE, fn::F16, 1>
+                          : fn::act_groups_kernel<MODE, fn::Bf16, 1>)
+                   : (f16 ? fn::act_groups_kernel<MODE, fn::F16, 2>
+                          : fn::act_groups_kernel<MODE, fn::Bf16, 2>);
 }
 
 template <class IO>
 fn::ActKernel act_row(int V) {
   return V == 1   ? fn::act_row_kernel<1, IO>
          : V == 2 ? fn::act_row_kernel<2, IO>
-                  : fn::act_row_kernel<4, IO>;
+         : V == 4 ? fn::act_row_kernel<4, IO>
+         : V == 8 ? fn::act_row_kernel<8, IO>
+                  : fn::act_row_kernel<16, IO>;
 }
 
 }  // namespace
@@ -522,7 +527,8 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
   const int sms = sm_count();
   if (sms <= 0) return FN_ERR_CUDA;
   if (mi.q == FN_FP8_PER_TOKEN) {
-    const int V = p.nvec <= 1024 ? 1 : p.nvec <= 2048 ? 2 : 4;
+    int V = 1;
+    while (p.nvec > 256 * V) V *= 2;
     const unsigned threads = (unsigned)round_up((p.nvec + V - 1) / V, 32);
     const unsigned grid = (unsigned)std::min<int64_t>(M, (int64_t)sms * 64);
     const int st = launch(mi.f16 ? act_row<fn::F16>(V) : act_row<fn::Bf16>(V), grid, threads, 0,
@@ -530,12 +536,14 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
     if (st == FN_OK) record(MX_VARIANT_SILU_ROW, grid, threads, V, 1);
     return st;
   }
-  const unsigned grid =
-      (unsigned)std::min<int64_t>((M * p.nvec + 255) / 256, (int64_t)sms * 64);
-  const int st = launch(mi.q == FN_MXFP4 ? act_groups<fn::MODE_MX>(mi.f16)
-                                         : act_groups<fn::MODE_G128>(mi.f16),
+  // two vectors a thread once every SM has eight blocks of one
+  const int vecs = M * p.nvec > (int64_t)sms * 8 * 256 ? 2 : 1;
+  const int64_t per = 256 * vecs;
+  const unsigned grid = (unsigned)std::min<int64_t>((M * p.nvec + per - 1) / per, (int64_t)sms * 256);
+  const int st = launch(mi.q == FN_MXFP4 ? act_groups<fn::MODE_MX>(mi.f16, vecs)
+                                         : act_groups<fn::MODE_G128>(mi.f16, vecs),
                         grid, 256, 0, stream, 1, tl_pdl != 0, p);
-  if (st == FN_OK) record(MX_VARIANT_SILU_GROUPS, grid, 256, 1, 1);
+  if (st == FN_OK) record(MX_VARIANT_SILU_GROUPS, grid, 256, vecs, 1);
   return st;
 }
 
