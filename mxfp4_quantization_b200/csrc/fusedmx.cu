@@ -114,13 +114,13 @@ EncodeTiled encoder() {
   return f;
 }
 
-// Scale tiles of the 32x4x4 tiling, 512 bytes each; boxes of two.
-bool scale_map(CUtensorMap* m, const void* s, int64_t tiles) {
+// Scale tiles of the 32x4x4 tiling, 512 bytes each; boxes of `box`.
+bool scale_map(CUtensorMap* m, const void* s, int64_t tiles, int box = 2) {
   EncodeTiled enc = encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {128, (cuuint64_t)tiles};
   const cuuint64_t strides[1] = {512};
-  const cuuint32_t boxes[2] = {128, 2};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box};
   const cuuint32_t elem[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(s), dims, strides, boxes,
              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -260,7 +260,7 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
       }
     }
     p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
-    p.x_bytes = p.pieces * 2 * kts * 512;
+    p.x_bytes = p.pieces * kts * fn::kMgXTile;
     // weights' tiles are taken as they are, unless a padding byte would be read
     if (!(flags & MX_B_SCALE_SWIZZLE) || groups & 1)
       p.w_bytes = (grouped ? E : 1) * ceil_div(N, 128) * kts * 512;
@@ -273,7 +273,7 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
     const int64_t steps = ceil_div(K, fn::kMgStageK), tiles = p.feat * p.pieces;
     while (p.split < 8 && tiles * p.split * 2 <= 2 * kSms && p.split * 4 <= steps) p.split *= 2;
   }
-  if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * 2 * kts > kMaxRows ||
+  if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * kts > kMaxRows / 8 ||
       (grouped ? E : 1) * ceil_div(N, 128) * kts > kMaxRows || ceil_div(M, 128) * kts > kMaxRows)
     return FN_ERR_UNSUPPORTED;
   *out = p;
@@ -345,7 +345,7 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   p.box = fn::kMgPairRows / 6;
   if (!code_map(&maps.x, a.codes ? static_cast<const void*>(a.codes) : q.a_q,
                 a.codes ? q.M : q.a_rows, q.K, p.box) ||
-      !scale_map(&maps.xs, a.x_tiles, plan.x_bytes / 512) ||
+      !scale_map(&maps.xs, a.x_tiles, plan.x_bytes / 512, 16) ||
       !scale_map(&maps.ws, a.w_tiles ? a.w_tiles : q.b_scale, tiles_w))
     return FN_ERR_CUDA;
   const int64_t items = std::max(plan.pieces * 2, a.w_tiles ? p.E * ceil_div(q.N, 128) : 0) *
