@@ -60,8 +60,12 @@ struct MGPTile {
   int e, f0, row0, n, piece;
 };
 
-// The tiles in order: expert, feature tile, row tile.
+// The tiles in order: expert, group of eight row tiles, feature tile, row tile.  The
+// 74 pairs then work on about 9 x 8 tiles at a time, whose operands stay in L2
+// (with all row tiles in one group 32768 x 4096 x 7168 read its 117 MB of rows once
+// per feature tile: 523 us against 463).
 struct MGPTiles {
+  static constexpr int kGroup = 8;
   const int* cum;  // [E + 1] row tiles before expert e   (offsets given)
   const int* lo;
   const int* cnt;
@@ -86,7 +90,10 @@ struct MGPTiles {
       } else {
         nt = (rows + tok - 1) / tok;
       }
-      const int f = rel / nt, m = rel - f * nt;
+      // groups of kGroup row tiles, all their feature tiles in turn
+      const int g = rel / (feat * kGroup) * kGroup, in = min(kGroup, nt - g);
+      rel -= g * feat;
+      const int f = rel / in, m = g + rel - f * in;
       const int h = mgp_height(rows, tok);
       o.e = e;
       o.f0 = f * kMgPairFeat;
