@@ -269,9 +269,11 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
     p.feat = ceil_div(N, fn::kMgFeat);
     p.tok = each <= 16 ? 16 : each <= 64 ? 64 : 128;
     p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
-    // few tiles: the blocks of a cluster share the K steps of one
+    // few tiles: the blocks of a cluster share the K steps of one, while all of them
+    // fit the GPU at once
     const int64_t steps = ceil_div(K, fn::kMgStageK), tiles = p.feat * p.pieces;
-    while (p.split < 8 && tiles * p.split * 2 <= 2 * kSms && p.split * 4 <= steps) p.split *= 2;
+    const int64_t fit = p.tok == 16 ? 2 * kSms : kSms;
+    while (p.split < 8 && tiles * p.split * 2 <= fit && p.split * 4 <= steps) p.split *= 2;
   }
   if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * kts > kMaxRows / 8 ||
       (grouped ? E : 1) * ceil_div(N, 128) * kts > kMaxRows || ceil_div(M, 128) * kts > kMaxRows)
@@ -307,10 +309,12 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   p.tok = plan.tok;
   p.pieces = (int)plan.pieces;
   p.split = plan.split;
+  while (1 << p.split_log2 < p.split) ++p.split_log2;
   const int sms = sm_count();
   if (sms <= 0) return FN_ERR_CUDA;
   const int table = grouped ? (3 * p.E + 1) * 4 : 0;
   const int64_t tiles_w = p.E * ceil_div(q.N, 128) * ceil_div(p.groups, 4);
+  p.w_tiles = (int)(tiles_w / p.E);
   const int64_t tiles_x = ceil_div(q.a_rows, 128) * ceil_div(p.groups, 4);
   const fn::MGInstance k = plan.pair ? fn::mg_pair() : fn::mg_pick(plan.tok);
   fn::MGMaps maps;

@@ -43,12 +43,6 @@ __device__ __forceinline__ void mg_table(const MGParams& p, int* table, int lane
   if (lane == 0) cum[0] = 0;
 }
 
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ uint4 ld_scales16(const uint8_t* p) {
   uint4 v;
   asm("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"

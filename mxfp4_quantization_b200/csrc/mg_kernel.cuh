@@ -45,8 +45,11 @@ struct MGShape {
   static constexpr int kColEnd = kColSx + 8;
   static constexpr int kCols = kColEnd <= 64 ? 64 : kColEnd <= 256 ? 256 : 512;
   static constexpr int kChunk = TOK >= 32 ? 32 : 16;  // columns the epilogue takes at once
+  // a split's partial sums of the smallest tile: [block][row / split][feature]
+  static constexpr bool kPush = TOK == 16;
+  static constexpr int kPushBytes = kPush ? TOK * kMgFeat * 4 : 0;
   // 1024 bytes: the operand tiles' alignment
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kSmem = kStages * kStage + kPushBytes + 1024;
   static_assert(kStages * kStage >= TOK * kMgFeat * 4, "a split's partial sums");
 };
 
@@ -62,11 +65,11 @@ struct MGTiles {
   const int* cum;  // [E + 1] tiles before expert e   (offsets given)
   const int* lo;   // [E] first row
   const int* cnt;  // [E] rows
-  int t, e, total, M, p_split;
+  int t, e, total, M, stride;
 
   __device__ MGTiles(const MGParams& p, const int* table)
-      : cum(table), lo(table + p.E + 1), cnt(table + 2 * p.E + 1), t(blockIdx.x / p.split), e(0),
-        M(p.M), p_split(p.split) {
+      : cum(table), lo(table + p.E + 1), cnt(table + 2 * p.E + 1), t(blockIdx.x >> p.split_log2), e(0),
+        M(p.M), stride(gridDim.x >> p.split_log2) {
     const int feat = (p.N + kMgFeat - 1) / kMgFeat;
     total = p.offsets ? cum[p.E] : feat * ((M + TOK - 1) / TOK);
     if (!p.offsets) cum = nullptr;
@@ -86,7 +89,7 @@ struct MGTiles {
     o.f0 = f * kMgFeat;
     o.row0 = first + m * TOK;
     o.n = min(TOK, rows - m * TOK);
-    t += gridDim.x / p_split;
+    t += stride;
     return true;
   }
 };
@@ -103,7 +106,8 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t tiles0 = (smem_addr(dyn) + 1023) & ~1023u;
   uint8_t* const tiles_p = dyn + (tiles0 - smem_addr(dyn));
-  int* table = reinterpret_cast<int*>(tiles_p + S::kStages * S::kStage);
+  int* table = reinterpret_cast<int*>(tiles_p + S::kStages * S::kStage + S::kPushBytes);
+  const uint32_t part0 = tiles0 + S::kStages * S::kStage;
   const uint32_t full = smem_addr(bars), sfull = full + 8 * S::kStages,
                  empty = sfull + 8 * S::kStages, tfull = empty + 8 * S::kStages,
                  tempty = tfull + 16, drain = tempty + 16;
@@ -136,16 +140,21 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // (known to be uniform)
+  if (S::kPush && p.split > 1) cluster_arrive_started();
   // a split's blocks share the K steps of their tile
   const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
-  const int all = (p.K + kMgStageK - 1) / kMgStageK;
-  const int kb0 = (int)((int64_t)all * rank / p.split);
-  const int kb1 = (int)((int64_t)all * (rank + 1) / p.split);
+  const int all = (p.K + kMgStageK - 1) / kMgStageK, shift = p.split_log2;
+  const int kb0 = all * (int)rank >> shift, kb1 = all * ((int)rank + 1) >> shift;
   const int kts = (p.groups + 3) >> 2;
   MGTiles<TOK> tiles(p, table);
   MGTile t;
 
+  // Warps 0 and 1 run their loops with all lanes and only issue from one: their
+  // operands then stay in uniform registers (inside a one-lane branch every
+  // instruction moved its descriptors there first: 630 cycles for the eight
+  // tcgen05 instructions of a K step).
+  const bool leader = elect_one();
   if (warp == 0) {
     // ---- operands -----------------------------------------------------------------------
     int s = 0, issued = 0;
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
       const int each = p.rows ? 4 : p.box;
       const int pieces = (t.n + each - 1) / each;
       const uint32_t codes = S::kWBytes + (uint32_t)(pieces * each) * 128;
-      const int ws0 = (int)(t.e * (p.w_scale_stride / 512)) + t.f0 / 128 * kts;
+      const int ws0 = t.e * p.w_tiles + t.f0 / 128 * kts;
       const int xs0 = t.row0 / 128 * kts;
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = mbar_wait<1>(empty + 8 * s, ph ^ 1, &stop);
@@ -177,19 +186,18 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
         const bool tw = p.w_mode == MG_SCALE_TMA || (p.w_mode == MG_SCALE_TMA_TAIL && !last);
         const bool tx = p.x_mode == MG_SCALE_TMA || (p.x_mode == MG_SCALE_TMA_TAIL && !last);
         const uint32_t bar = full + 8 * s;
-        if (lane == 0) {
+        if (leader) {
           mbar_expect_tx(bar, codes + (tw ? S::kScaleBytes : 0) + (tx ? S::kScaleBytes : 0));
           tma_load<1>(w_tile(s), &maps.w, kb * 128, wrow, bar);
           if (tw) tma_load<1>(sw_tile(s), &maps.ws, 0, ws0 + 2 * kb, bar);
           if (tx) tma_load<1>(sx_tile(s), &maps.xs, 0, xs0 + 2 * kb, bar);
+          if (!p.rows)
+            for (int i = 0; i < pieces; ++i)
+              tma_load<1>(x_tile(s) + i * p.box * 128, &maps.x, kb * 128, t.row0 + i * p.box, bar);
         }
-        __syncwarp();
-        if (lane < pieces) {
-          if (p.rows)
-            tma_gather4<1>(x_tile(s) + lane * 512, &maps.x, kb * 128, src, bar);
-          else
-            tma_load<1>(x_tile(s) + lane * p.box * 128, &maps.x, kb * 128, t.row0 + lane * p.box,
-                        bar);
+        if (p.rows) {
+          __syncwarp();
+          if (lane < pieces) tma_gather4<1>(x_tile(s) + lane * 512, &maps.x, kb * 128, src, bar);
         }
         ++issued;
         if (++s == S::kStages) s = 0, ph ^= 1;
@@ -204,33 +212,45 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
     }
   } else if (warp == 1) {
     // ---- MMA ----------------------------------------------------------------------------
-    if (lane == 0) {
-      int s = 0, i = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (; ok && tiles.next(t); ++i) {
-        const int acc = i & 1;
-        const uint32_t d = tmem + acc * TOK;
-        const int n16 = (t.n + 15) / 16 * 16;
-        const uint32_t id0 = mxf4_idesc(kMgFeat, n16, 0), id1 = mxf4_idesc(kMgFeat, n16, 1);
-        ok = mbar_wait<1>(tempty + 8 * acc, ((i >> 1) & 1) ^ 1, &stop);
+    int s = 0, i = 0, fenced = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (; ok && tiles.next(t); ++i) {
+      const int acc = i & 1;
+      const uint32_t d = tmem + acc * TOK;
+      const int n16 = (t.n + 15) / 16 * 16;
+      const uint32_t id0 = mxf4_idesc(kMgFeat, n16, 0), id1 = mxf4_idesc(kMgFeat, n16, 1);
+      ok = mbar_wait<1>(tempty + 8 * acc, ((i >> 1) & 1) ^ 1, &stop);
+      tc_fence_after();
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        ok = mbar_wait<1>(full + 8 * s, ph, &stop);
+        // The fence for the scale warps' writes is made here, where no loads are in
+        // flight: it waits for a thread's own, and the scale warps always have
+        // some (with the fence in those warps a K step took 1.2 us).  It covers
+        // every stage whose scales are there already.
+        if (ok && scale_warps > 0 && fenced == 0) {
+          ok = mbar_wait<1>(sfull + 8 * s, ph, &stop);
+          int n = s;
+          uint32_t nph = ph;
+          do {
+            ++fenced;
+            if (++n == S::kStages) n = 0, nph ^= 1;
+          } while (fenced < S::kStages &&
+                   __all_sync(0xffffffffu, mbar_test(sfull + 8 * n, nph)));
+          fence_async_smem();
+        }
+        if (!ok) break;
+        --fenced;
         tc_fence_after();
-        for (int kb = kb0; ok && kb < kb1; ++kb) {
-          ok = mbar_wait<1>(full + 8 * s, ph, &stop) &&
-               (scale_warps == 0 || mbar_wait<1>(sfull + 8 * s, ph, &stop));
-          if (!ok) break;
-          // The fence for the scale warps' writes is made here, where no loads are
-          // in flight: it waits for a thread's own, and the scale warps always
-          // have some (with the fence in those warps a K step took 1.2 us).
-          if (scale_warps > 0) fence_async_smem();
-          tc_fence_after();
+        const int mmas = min(4, (p.K - kb * kMgStageK + 63) / 64);
+        const uint64_t a = operand_desc(w_tile(s)), b = operand_desc(x_tile(s));
+        const uint64_t sw = scale_desc(sw_tile(s)), sx = scale_desc(sx_tile(s));
+        if (leader) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            tc_copy_scales<1>(tmem + S::kColSw + 4 * h, scale_desc(sw_tile(s) + 512 * h));
-            tc_copy_scales<1>(tmem + S::kColSx + 4 * h, scale_desc(sx_tile(s) + 512 * h));
+            tc_copy_scales<1>(tmem + S::kColSw + 4 * h, sw + 32 * h);
+            tc_copy_scales<1>(tmem + S::kColSx + 4 * h, sx + 32 * h);
           }
-          const uint64_t a = operand_desc(w_tile(s)), b = operand_desc(x_tile(s));
-          const int mmas = min(4, (p.K - kb * kMgStageK + 63) / 64);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (j < mmas)
@@ -238,14 +258,17 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
                              tmem + S::kColSw + 4 * (j / 2), tmem + S::kColSx + 4 * (j / 2),
                              kb > kb0 || j > 0);
           tc_commit<1>(empty + 8 * s);
-          if (++s == S::kStages) s = 0, ph ^= 1;
         }
-        if (ok) tc_commit<1>(tfull + 8 * acc);
+        __syncwarp();
+        if (++s == S::kStages) s = 0, ph ^= 1;
       }
-      if (!ok) {  // MMAs in flight end before the block goes
-        tc_commit<1>(drain);
-        for (int n = 0; n < kWaitTries && !mbar_try<1>(drain, 0); ++n) {
-        }
+      if (ok && leader) tc_commit<1>(tfull + 8 * acc);
+      __syncwarp();
+    }
+    if (!ok) {  // MMAs in flight end before the block goes
+      if (leader) tc_commit<1>(drain);
+      __syncwarp();
+      for (int n = 0; n < kWaitTries && !mbar_try<1>(drain, 0); ++n) {
       }
     }
   } else if (warp < 4) {
@@ -329,6 +352,7 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
     // ---- epilogue ---------------------------------------------------------------------------
     const int quad = warp & 3;  // the TMEM lanes a warp can read
     constexpr int C = S::kChunk;
+    if (S::kPush && p.split > 1) cluster_wait_started();
     bool ok = true;
     for (int i = 0; tiles.next(t); ++i) {
       const int acc = i & 1;
@@ -351,7 +375,14 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
               if (!((keep >> q) & 1)) v[q] = 0;
           }
         }
-        if (p.split > 1) {  // this block's partial sums, over the operand tiles (all read)
+        if (p.split > 1 && S::kPush) {  // to the block that sums the row
+          const uint32_t to = part0 + (rank * (TOK / p.split) * kMgFeat + quad * 32 + lane) * 4;
+#pragma unroll
+          for (int q = 0; q < C; ++q)
+            if (c + q < t.n)
+              st_cluster(cluster_map(to + ((c + q) >> shift) * kMgFeat * 4, (c + q) & (p.split - 1)),
+                         __uint_as_float(v[q]));
+        } else if (p.split > 1) {  // this block's partial sums, over the operand tiles (all read)
           float* part = reinterpret_cast<float*>(tiles_p) + quad * 32 + lane;
 #pragma unroll
           for (int q = 0; q < C; ++q)
@@ -368,22 +399,33 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
   __syncwarp();
   tc_fence_before();
   if (p.split > 1) {
+    if (S::kPush && warp < 4) cluster_wait_started();
     // One tile a split.  Block r sums rows r, r + split, ... over the blocks, in
-    // order.
+    // order.  The smallest tile's partial sums were pushed there (one barrier of
+    // the cluster); the others are fetched, and the blocks wait for each other
+    // again before they go.
     cluster_sync_all();
     MGTiles<TOK> again(p, table);
     if (again.next(t)) {
       const int f = threadIdx.x & (kMgFeat - 1);
-      const uint32_t part = tiles0 + f * 4;
       for (int j = (int)rank + p.split * (threadIdx.x / kMgFeat); j < t.n;
            j += p.split * (kMgThreads / kMgFeat)) {
-        float sum = 0.f;
-        for (int q = 0; q < p.split; ++q)
-          sum += ld_cluster(cluster_map(part + j * kMgFeat * 4, q));
+        const int slot = S::kPush ? j / p.split : j;
+        const int next = TOK / p.split * kMgFeat * 4;  // from a block's sums to the next one's
+        const uint32_t at = (S::kPush ? part0 : tiles0) + (slot * kMgFeat + f) * 4;
+        float v[8], sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.split)
+            v[q] = S::kPush ? ld_shared(at + q * next)
+                            : ld_cluster(cluster_map(at, q));
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.split) sum += v[q];
         if (t.f0 + f < p.N) mg_store_one(p, sum, (int64_t)t.row0 + j, t.f0 + f);
       }
     }
-    cluster_sync_all();
+    if (!S::kPush) cluster_sync_all();
   } else {
     __syncthreads();
   }

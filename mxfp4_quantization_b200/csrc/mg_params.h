@@ -40,7 +40,8 @@ struct MGParams {
   int tok;                  // pair kernel: rows of a tile, a multiple of 16
   int box;                  // rows of a token TMA box (1: gather)
   int pieces;               // row tiles there can be, over all experts
-  int split;                // blocks (a cluster) that share a tile's K steps
+  int split, split_log2;    // blocks (a cluster) that share a tile's K steps: 1, 2, 4 or 8
+  int w_tiles;              // 512-byte scale tiles of one expert's weights
 };
 
 constexpr int kMgPairFeat = 256;     // features of a pair's tile

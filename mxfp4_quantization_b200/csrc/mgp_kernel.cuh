@@ -152,12 +152,14 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // (known to be uniform)
   const int steps = (p.K + kMgStageK - 1) / kMgStageK;
   const int kts = (p.groups + 3) >> 2;
   MGPTiles tiles(p, table);
   MGPTile t;
 
+  // warps 0 and 1 loop with all lanes and issue from one (as in mg_kernel.cuh)
+  const bool leader = elect_one();
   if (warp == 0) {
     // ---- operands: each block its own features' and its half of the rows' codes, and
     // all scales that its MMA half reads; all bytes count on the first block's
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
         ok = mbar_wait<2>(empty + 8 * s, ph ^ 1, &stop);
         if (!ok) break;
         const uint32_t bar = cluster_map(full + 8 * s, 0);
-        if (lane == 0) {
+        if (leader) {
           if (rank == 0) mbar_expect_tx(full + 8 * s, bytes);
           tma_load<2>(w_tile(s), &maps.w, kb * 128, t.e * p.N + f0, bar);
           tma_load<2>(sw_tile(s), &maps.ws, 0, ws0 + 2 * kb, bar);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
     }
   } else if (warp == 1) {
     // ---- MMA ----------------------------------------------------------------------------
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int s = 0, i = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -219,27 +221,32 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
           ok = mbar_wait<2>(full + 8 * s, ph, &stop);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tc_copy_scales<2>(tmem + S::kColSw + 4 * h, scale_desc(sw_tile(s) + 512 * h));
-            tc_copy_rows<2>(tmem + S::kColSx + 8 * h,
-                            scale_desc(sx_tile(s) + kMgXTile * h, kMgXTile / 2));
-          }
-          const uint64_t a = operand_desc(w_tile(s)), b = operand_desc(x_tile(s));
           const int mmas = min(4, (p.K - kb * kMgStageK + 63) / 64);
+          const uint64_t a = operand_desc(w_tile(s)), b = operand_desc(x_tile(s));
+          const uint64_t sw = scale_desc(sw_tile(s)), sx = scale_desc(sx_tile(s), kMgXTile / 2);
+          if (leader) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < mmas)
-              tc_mma_mxf4<2>(d, a + 2 * j, b + 2 * j, j & 1 ? id1 : id0,
-                             tmem + S::kColSw + 4 * (j / 2), tmem + S::kColSx + 8 * (j / 2),
-                             kb > 0 || j > 0);
-          tc_commit<2>(empty + 8 * s);
+            for (int h = 0; h < 2; ++h) {
+              tc_copy_scales<2>(tmem + S::kColSw + 4 * h, sw + 32 * h);
+              tc_copy_rows<2>(tmem + S::kColSx + 8 * h, sx + kMgXTile / 16 * h);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < mmas)
+                tc_mma_mxf4<2>(d, a + 2 * j, b + 2 * j, j & 1 ? id1 : id0,
+                               tmem + S::kColSw + 4 * (j / 2), tmem + S::kColSx + 8 * (j / 2),
+                               kb > 0 || j > 0);
+            tc_commit<2>(empty + 8 * s);
+          }
+          __syncwarp();
           if (++s == S::kStages) s = 0, ph ^= 1;
         }
-        if (ok) tc_commit<2>(tfull + 8 * acc);
+        if (ok && leader) tc_commit<2>(tfull + 8 * acc);
+        __syncwarp();
       }
       if (!ok) {  // MMAs in flight end before the blocks go
-        tc_commit<2>(drain);
+        if (leader) tc_commit<2>(drain);
+        __syncwarp();
         for (int n = 0; n < kWaitTries && !mbar_try<2>(drain, 0); ++n) {
         }
       }
