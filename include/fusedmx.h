@@ -52,9 +52,10 @@ extern "C" {
 
 #define MX_MAX_EXPERTS 1024
 #define MX_MAX_TOP 32
-/* Products of at most this many rows (an average of that many per expert) need
- * no workspace. */
-#define MX_SMALL_ROWS 128
+/* Products of at most this many rows, and grouped products of at most that many
+ * per expert on average (R <= MX_SMALL_EXPERT_ROWS * E), need no workspace. */
+#define MX_SMALL_ROWS 64
+#define MX_SMALL_EXPERT_ROWS 16
 
 /*
  * Product of two MXFP4 operands (a linear layer on quantized rows):

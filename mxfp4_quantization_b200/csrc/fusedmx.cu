@@ -246,7 +246,11 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
   const int64_t each = grouped ? ceil_div(M, E) : M;
   const int64_t more = grouped ? std::min(E, M) : 0;  // a partly filled tile an expert
   const int64_t groups = K / 32, kts = ceil_div(groups, 4);
-  p.pair = each > MX_SMALL_ROWS;
+  // Pairs of blocks from here on.  Measured, us a call of single blocks / of pairs,
+  // 8192 x 7168: 64 rows 14.2 / 15.2, 96 rows 16.3 / 15.6, 128 rows 18.4 / 15.7;
+  // experts of 4096 x 7168 with 32 rows on average 256 / 177 (64 experts), 39 / 34
+  // (8 experts); 2048 x 2048 with 50 rows 12.0 / 13.0 (4 experts).
+  p.pair = each > (grouped ? MX_SMALL_EXPERT_ROWS : MX_SMALL_ROWS);
   if (p.pair) {
     p.feat = ceil_div(N, fn::kMgPairFeat);
     p.tok = fn::kMgPairRows;
@@ -267,7 +271,7 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
     if (gather) p.code_bytes = M * (K / 2);
   } else {
     p.feat = ceil_div(N, fn::kMgFeat);
-    p.tok = each <= 16 ? 16 : each <= 64 ? 64 : 128;
+    p.tok = each <= 16 ? 16 : 64;
     p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
     // few tiles: the blocks of a cluster share the K steps of one, while all of them
     // fit the GPU at once

@@ -10,7 +10,7 @@ MGInstance instance() {
 }
 
 MGInstance mg_pick(int tok) {
-  return tok <= 16 ? instance<16>() : tok <= 64 ? instance<64>() : instance<128>();
+  return tok <= 16 ? instance<16>() : instance<64>();
 }
 
 MGInstance mg_pair() { return {mgp_kernel, kMgPairRows, MGPShape::kSmem, 1}; }

@@ -11,8 +11,8 @@
 // call has one row or an expert's row range ends inside a tile.  A feature is
 // then a TMEM lane and a row a TMEM column.
 //
-// This kernel takes calls of few rows (an expert, or a product, of up to 128); the
-// pair kernel (mgp_kernel.cuh) the others.  Persistent blocks, one role per
+// This kernel takes calls of few rows (a product of up to 64, experts of 16 on
+// average); the pair kernel (mgp_kernel.cuh) the others.  Persistent blocks, one role per
 // warp:
 //   warp 0      TMA: the weight tile and the row tile of each K step of 256
 //               elements (128 bytes a row, 128-byte swizzle; rows by index
@@ -37,7 +37,7 @@ struct MGShape {
   static constexpr int kScaleBytes = 2 * 512;  // of either operand
   static constexpr int kStage = kWBytes + kXBytes + 2 * kScaleBytes;
   // two blocks fit an SM for the smallest tile
-  static constexpr int kStages = TOK >= 128 ? 6 : TOK >= 64 ? 8 : 5;
+  static constexpr int kStages = TOK >= 64 ? 8 : 5;
   static constexpr int kPerSm = TOK >= 64 ? 1 : 2;
   // TMEM: two accumulators, then the scales (4 columns per 128 elements each)
   static constexpr int kColSw = 2 * TOK;
@@ -45,12 +45,18 @@ struct MGShape {
   static constexpr int kColEnd = kColSx + 8;
   static constexpr int kCols = kColEnd <= 64 ? 64 : kColEnd <= 256 ? 256 : 512;
   static constexpr int kChunk = TOK >= 32 ? 32 : 16;  // columns the epilogue takes at once
+  static constexpr int kXLaneRows = (TOK + 31) / 32;  // rows whose scales a lane brings
   // a split's partial sums of the smallest tile: [block][row / split][feature]
   static constexpr bool kPush = TOK == 16;
   static constexpr int kPushBytes = kPush ? TOK * kMgFeat * 4 : 0;
   // 1024 bytes: the operand tiles' alignment
   static constexpr int kSmem = kStages * kStage + kPushBytes + 1024;
   static_assert(kStages * kStage >= TOK * kMgFeat * 4, "a split's partial sums");
+};
+
+template <int R>
+struct MGRows {
+  static constexpr int value = R;
 };
 
 struct MGTile {
@@ -149,6 +155,84 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
   const int kts = (p.groups + 3) >> 2;
   MGTiles<TOK> tiles(p, table);
   MGTile t;
+
+  // The scales of one operand, for warps 2 and 3.
+  auto scale_role = [&](auto lane_rows, bool is_x) {
+    constexpr int R = decltype(lane_rows)::value;
+    const int mode = is_x ? p.x_mode : p.w_mode;
+    const bool wide = is_x ? p.x_wide : p.w_wide;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    while (ok && tiles.next(t)) {
+      const uint8_t* base = is_x ? p.x_scale : p.w_scale + t.e * p.w_scale_stride;
+      const uint8_t* src[R];
+      int64_t row[R];
+      bool in[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int j = i * 32 + lane;
+        int v;
+        if (is_x) {
+          in[i] = j < t.n;
+          v = t.row0 + j;
+          if (p.rows && in[i]) {
+            v = p.rows[v];
+            in[i] = (unsigned)v < (unsigned)p.x_rows;
+          }
+        } else {
+          v = t.f0 + j;
+          in[i] = v < p.N;
+        }
+        row[i] = in[i] ? v : 0;
+        src[i] = base + row[i] * p.groups;
+      }
+      // the chunk of 16 groups with K steps 2 c, 2 c + 1
+      auto fetch = [&](uint4 (&b)[R], int c) {
+        const bool use = 2 * c < kb1 && (mode == MG_SCALE_WARP || 2 * c + 2 >= all);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          b[i] = !in[i] || !use          ? make_uint4(0, 0, 0, 0)
+                 : mode == MG_SCALE_WARP ? mg_scales(src[i], c, p.groups, wide)
+                                         : mg_tiled_scales(base, row[i], c, p.groups);
+      };
+      auto emit = [&](const uint4 (&b)[R], int c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kb = 2 * c + h;
+          if (kb >= kb0 && kb < kb1 && ok) {
+            ok = mbar_wait<1>(empty + 8 * s, ph ^ 1, &stop);
+            if (ok && (mode == MG_SCALE_WARP || kb == all - 1)) {
+              const uint32_t dst = (is_x ? sx_tile(s) : sw_tile(s)) + lane * 16;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int w = 2 * h + k;
+                // (rows beyond the lane's are beyond the tile: their words are not read)
+                st_shared_words(dst + 512 * k, word(b[0], w), word(b[R > 1 ? 1 : 0], w),
+                                word(b[R > 2 ? 2 : 0], w), word(b[R > 3 ? 3 : 0], w));
+              }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(sfull + 8 * s);
+            if (++s == S::kStages) s = 0, ph ^= 1;
+          }
+        }
+      };
+      // three buffers by name: a copy from one to the next would wait for its load
+      const int c0 = kb0 / 2;
+      uint4 b0[R], b1[R], b2[R];
+      fetch(b0, c0);
+      fetch(b1, c0 + 1);
+      for (int c = c0; 2 * c < kb1 && ok; c += 3) {
+        fetch(b2, c + 2);
+        emit(b0, c);
+        fetch(b0, c + 3);
+        emit(b1, c + 1);
+        fetch(b1, c + 4);
+        emit(b2, c + 2);
+      }
+    }
+  };
 
   // Warps 0 and 1 run their loops with all lanes and only issue from one: their
   // operands then stay in uniform registers (inside a one-lane branch every
@@ -273,81 +357,9 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
     }
   } else if (warp < 4) {
     // ---- scales ---------------------------------------------------------------------------
-    const bool is_x = warp == 2;
-    const int mode = is_x ? p.x_mode : p.w_mode;
-    if (mode != MG_SCALE_TMA) {
-      const bool wide = is_x ? p.x_wide : p.w_wide;
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      while (ok && tiles.next(t)) {
-        const uint8_t* base = is_x ? p.x_scale : p.w_scale + t.e * p.w_scale_stride;
-        const uint8_t* src[4];
-        int64_t row[4];
-        bool in[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = i * 32 + lane;
-          int v;
-          if (is_x) {
-            in[i] = j < t.n;
-            v = t.row0 + j;
-            if (p.rows && in[i]) {
-              v = p.rows[v];
-              in[i] = (unsigned)v < (unsigned)p.x_rows;
-            }
-          } else {
-            v = t.f0 + j;
-            in[i] = v < p.N;
-          }
-          row[i] = in[i] ? v : 0;
-          src[i] = base + row[i] * p.groups;
-        }
-        // the chunk of 16 groups with K steps 2 c, 2 c + 1
-        auto fetch = [&](uint4 (&b)[4], int c) {
-          const bool use = 2 * c < kb1 && (mode == MG_SCALE_WARP || 2 * c + 2 >= all);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            b[i] = !in[i] || !use          ? make_uint4(0, 0, 0, 0)
-                   : mode == MG_SCALE_WARP ? mg_scales(src[i], c, p.groups, wide)
-                                           : mg_tiled_scales(base, row[i], c, p.groups);
-        };
-        auto emit = [&](const uint4 (&b)[4], int c) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int kb = 2 * c + h;
-            if (kb >= kb0 && kb < kb1 && ok) {
-              ok = mbar_wait<1>(empty + 8 * s, ph ^ 1, &stop);
-              if (ok && (mode == MG_SCALE_WARP || kb == all - 1)) {
-                const uint32_t dst = (is_x ? sx_tile(s) : sw_tile(s)) + lane * 16;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512 * k),
-                               "r"(word(b[0], 2 * h + k)), "r"(word(b[1], 2 * h + k)),
-                               "r"(word(b[2], 2 * h + k)), "r"(word(b[3], 2 * h + k))
-                               : "memory");
-              }
-              __syncwarp();
-              if (ok && lane == 0) mbar_arrive(sfull + 8 * s);
-              if (++s == S::kStages) s = 0, ph ^= 1;
-            }
-          }
-        };
-        // three buffers by name: a copy from one to the next would wait for its load
-        const int c0 = kb0 / 2;
-        uint4 b0[4], b1[4], b2[4];
-        fetch(b0, c0);
-        fetch(b1, c0 + 1);
-        for (int c = c0; 2 * c < kb1 && ok; c += 3) {
-          fetch(b2, c + 2);
-          emit(b0, c);
-          fetch(b0, c + 3);
-          emit(b1, c + 1);
-          fetch(b1, c + 4);
-          emit(b2, c + 2);
-        }
-      }
-    }
+    // rows a lane brings: the tile's, or the weights' 128
+    if (warp == 2 && p.x_mode != MG_SCALE_TMA) scale_role(MGRows<S::kXLaneRows>(), true);
+    if (warp == 3 && p.w_mode != MG_SCALE_TMA) scale_role(MGRows<4>(), false);
   } else {
     // ---- epilogue ---------------------------------------------------------------------------
     const int quad = warp & 3;  // the TMEM lanes a warp can read
@@ -408,21 +420,26 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
     MGTiles<TOK> again(p, table);
     if (again.next(t)) {
       const int f = threadIdx.x & (kMgFeat - 1);
-      for (int j = (int)rank + p.split * (threadIdx.x / kMgFeat); j < t.n;
-           j += p.split * (kMgThreads / kMgFeat)) {
-        const int slot = S::kPush ? j / p.split : j;
-        const int next = TOK / p.split * kMgFeat * 4;  // from a block's sums to the next one's
-        const uint32_t at = (S::kPush ? part0 : tiles0) + (slot * kMgFeat + f) * 4;
-        float v[8], sum = 0.f;
+      const int half = threadIdx.x / kMgFeat, next = TOK / p.split * kMgFeat * 4;
+      constexpr int R = TOK / 16;  // rows whose loads are in flight together
+      for (int j0 = 0; j0 << shift < t.n; j0 += 2 * R) {  // slots of this block's rows
+        float sum[R];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.split)
-            v[q] = S::kPush ? ld_shared(at + q * next)
-                            : ld_cluster(cluster_map(at, q));
+        for (int r = 0; r < R; ++r) sum[r] = 0.f;
+        for (int q = 0; q < p.split; ++q) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.split) sum += v[q];
-        if (t.f0 + f < p.N) mg_store_one(p, sum, (int64_t)t.row0 + j, t.f0 + f);
+          for (int r = 0; r < R; ++r) {
+            const int slot = j0 + half * R + r, j = (slot << shift) + (int)rank;
+            if (j < t.n)
+              sum[r] += S::kPush ? ld_shared(part0 + q * next + (slot * kMgFeat + f) * 4)
+                                 : ld_cluster(cluster_map(tiles0 + (j * kMgFeat + f) * 4, q));
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int j = ((j0 + half * R + r) << shift) + (int)rank;
+          if (j < t.n && t.f0 + f < p.N) mg_store_one(p, sum[r], (int64_t)t.row0 + j, t.f0 + f);
+        }
       }
     }
     if (!S::kPush) cluster_sync_all();

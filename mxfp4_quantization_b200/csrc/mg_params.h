@@ -73,7 +73,7 @@ struct MGInstance {
   int per_sm;    // blocks an SM holds
 };
 
-// The single-block instance for a token tile of `tok` rows (16, 64 or 128), and
+// The single-block instance for a token tile of `tok` rows (16 or 64), and
 // the pair kernel with the kernel that arranges its scales.
 using MGArrangeKernel = void (*)(const MGParams, const MGArrange);
 MGInstance mg_pick(int tok);

@@ -32,7 +32,8 @@ MX_A_SCALE_SWIZZLE = 0x10
 MX_B_SCALE_SWIZZLE = 0x20
 MX_MAX_EXPERTS = 1024
 MX_MAX_TOP = 32
-MX_SMALL_ROWS = 128
+MX_SMALL_ROWS = 64
+MX_SMALL_EXPERT_ROWS = 16
 
 MX_VARIANT_NONE = 0
 MX_VARIANT_GEMM = 1
@@ -331,7 +332,7 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     out, f, ldo = _product_out(out, out_dtype, R, N, dev)
     flags |= f
     ws = None
-    if R > MX_SMALL_ROWS * E:
+    if R > MX_SMALL_EXPERT_ROWS * E:
         ws = _workspace(mx_grouped_gemm_workspace_bytes(R, E, N, 2 * half, flags,
                                                         int(rows is not None)), workspace, dev)
     st = _call(_lib.mx_grouped_gemm, dev, a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
