@@ -7,9 +7,6 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
-#include <map>
-#include <mutex>
-#include <utility>
 
 #include "fusedmx.h"
 #include "act_kernel.cuh"
@@ -140,24 +137,28 @@ bool code_map(CUtensorMap* m, const void* q, int64_t rows, int64_t K, int box) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of a kernel, allowed once per kernel and device (function
-// attributes belong to a device's context).
-bool allow_smem(const void* k, int bytes) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> done;
+// Shared memory of a product kernel (`id`: its place in the record), allowed once per
+// kernel and device (function attributes belong to a device's context).  Plain
+// atomics: nothing here can throw through the C entries, and two threads that meet
+// set the same attribute twice.
+bool allow_smem(const fn::MGInstance& k, int bytes) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> done[fn::kMgInstances][kDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     (void)cudaGetLastError();
     return false;
   }
-  std::lock_guard<std::mutex> lock(mu);
-  int& have = done[std::make_pair(k, dev)];
-  if (have >= bytes) return true;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+  std::atomic<int>* have = dev >= 0 && dev < kDevices ? &done[k.id][dev] : nullptr;
+  if (have && have->load(std::memory_order_acquire) >= bytes) return true;
+  // the most that any call of the kernel asks for, so that it is set once
+  const int most = std::max(bytes, k.smem + (3 * MX_MAX_EXPERTS + 1) * 4);
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(k.kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
     (void)cudaGetLastError();
     return false;
   }
-  have = bytes;
+  if (have) have->store(most, std::memory_order_release);
   return true;
 }
 
@@ -324,10 +325,10 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   fn::MGMaps maps;
   std::memset(&maps, 0, sizeof maps);
   if (!code_map(&maps.w, q.b_q, p.E * q.N, q.K, fn::kMgFeat) ||
-      !allow_smem(reinterpret_cast<const void*>(k.kernel), k.smem + table))
+      !allow_smem(k, k.smem + table))
     return FN_ERR_CUDA;
   if (!plan.pair) {
-    p.box = q.rows ? 1 : std::min(plan.tok, 64);
+    p.box = q.rows ? 1 : plan.tok;
     if (!code_map(&maps.x, q.a_q, q.a_rows, q.K, p.box) ||
         (p.x_mode != fn::MG_SCALE_WARP && !scale_map(&maps.xs, q.a_scale, tiles_x)) ||
         (p.w_mode != fn::MG_SCALE_WARP && !scale_map(&maps.ws, q.b_scale, tiles_w)))

@@ -4,16 +4,16 @@
 
 namespace fn {
 
-template <int TOK>
+template <int TOK, int ID>
 MGInstance instance() {
-  return {mg_kernel<TOK>, TOK, MGShape<TOK>::kSmem, MGShape<TOK>::kPerSm};
+  return {mg_kernel<TOK>, TOK, MGShape<TOK>::kSmem, MGShape<TOK>::kPerSm, ID};
 }
 
 MGInstance mg_pick(int tok) {
-  return tok <= 16 ? instance<16>() : instance<64>();
+  return tok <= 16 ? instance<16, 0>() : instance<64, 1>();
 }
 
-MGInstance mg_pair() { return {mgp_kernel, kMgPairRows, MGPShape::kSmem, 1}; }
+MGInstance mg_pair() { return {mgp_kernel, kMgPairRows, MGPShape::kSmem, 1, 2}; }
 
 MGArrangeKernel mg_arrange() { return mgp_arrange_kernel; }
 

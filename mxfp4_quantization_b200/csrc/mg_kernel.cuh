@@ -90,7 +90,7 @@ struct MGTiles {
       first = lo[e];
     }
     const int nt = (rows + TOK - 1) / TOK;
-    const int f = rel / nt, m = rel - f * nt;
+    const int f = nt == 1 ? rel : rel / nt, m = rel - f * nt;
     o.e = e;
     o.f0 = f * kMgFeat;
     o.row0 = first + m * TOK;
@@ -124,29 +124,37 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
   auto sx_tile = [&](int s) { return sw_tile(s) + S::kScaleBytes; };
   const int scale_warps = (p.x_mode != MG_SCALE_TMA) + (p.w_mode != MG_SCALE_TMA);
 
-  if (threadIdx.x == 0) {
-    stop = 0;
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(sfull + 8 * s, max(1, scale_warps));
-      mbar_init(empty + 8 * s, 1);
+  // Warp 0 sets the barriers up (one a lane), makes the tile table and goes on to
+  // its loads; the others wait for that and for the TMEM allocation.
+  if (warp == 0) {
+    if (lane == 0) {
+      stop = 0;
+      tma_prefetch_map(&maps.w);
+      tma_prefetch_map(&maps.x);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull + 8 * b, 1);
-      mbar_init(tempty + 8 * b, 4);
+    constexpr int kBars = 3 * S::kStages + 5;
+    static_assert(kBars <= 32, "a barrier a lane");
+    if (lane < kBars) {
+      const int s = lane / S::kStages;  // 0 full, 1 sfull, 2 empty, then tfull, tempty, drain
+      const int last = lane - 3 * S::kStages;
+      mbar_init(full + 8 * lane, s == 1                     ? max(1, scale_warps)
+                                 : last == 2 || last == 3 ? 4
+                                                            : 1);
     }
-    mbar_init(drain, 1);
     fence_async_smem();
-    tma_prefetch_map(&maps.x);
-    tma_prefetch_map(&maps.w);
   }
   if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), S::kCols);
   pdl_enter();
   if (p.offsets && warp == 0) mg_table(p, table, lane, TOK, (p.N + kMgFeat - 1) / kMgFeat, p.pieces);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // (known to be uniform)
+  if (warp == 0) {
+    __syncwarp();
+    named_arrive<1>(kMgThreads);
+  } else {
+    tc_fence_before();
+    named_sync<1>(kMgThreads);
+    tc_fence_after();
+  }
+  const uint32_t tmem = warp == 0 ? 0 : __shfl_sync(0xffffffffu, tmem_slot, 0);  // (uniform)
   if (S::kPush && p.split > 1) cluster_arrive_started();
   // a split's blocks share the K steps of their tile
   const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
@@ -258,9 +266,8 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
         }
         src = make_int4(r[0], r[1], r[2], r[3]);
       }
-      const int each = p.rows ? 4 : p.box;
-      const int pieces = (t.n + each - 1) / each;
-      const uint32_t codes = S::kWBytes + (uint32_t)(pieces * each) * 128;
+      const int pieces = (t.n + 3) / 4;  // rows by index come four at a time
+      const uint32_t codes = S::kWBytes + (p.rows ? pieces * 512 : S::kXBytes);
       const int ws0 = t.e * p.w_tiles + t.f0 / 128 * kts;
       const int xs0 = t.row0 / 128 * kts;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -275,9 +282,7 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
           tma_load<1>(w_tile(s), &maps.w, kb * 128, wrow, bar);
           if (tw) tma_load<1>(sw_tile(s), &maps.ws, 0, ws0 + 2 * kb, bar);
           if (tx) tma_load<1>(sx_tile(s), &maps.xs, 0, xs0 + 2 * kb, bar);
-          if (!p.rows)
-            for (int i = 0; i < pieces; ++i)
-              tma_load<1>(x_tile(s) + i * p.box * 128, &maps.x, kb * 128, t.row0 + i * p.box, bar);
+          if (!p.rows) tma_load<1>(x_tile(s), &maps.x, kb * 128, t.row0, bar);
         }
         if (p.rows) {
           __syncwarp();

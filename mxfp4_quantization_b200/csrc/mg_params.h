@@ -71,7 +71,9 @@ struct MGInstance {
   int tok;       // token rows of a tile
   int smem;      // dynamic shared memory without the tile table
   int per_sm;    // blocks an SM holds
+  int id;        // 0 .. kMgInstances - 1
 };
+constexpr int kMgInstances = 3;
 
 // The single-block instance for a token tile of `tok` rows (16 or 64), and
 // the pair kernel with the kernel that arranges its scales.
