@@ -589,9 +589,10 @@ int mx_combine(const void* y, int64_t R, const int32_t* pos, const float* weight
   const unsigned threads = (unsigned)std::min<int64_t>(256, round_up(p.n, 32));
   p.per_row = (p.n + (int)threads - 1) / (int)threads;
   const unsigned grid = (unsigned)(T * p.per_row);
-  fn::CombineKernel kern = wide ? (f16 ? fn::combine_kernel<fn::F16> : fn::combine_kernel<fn::Bf16>)
-                                : (f16 ? fn::combine_narrow_kernel<fn::F16>
-                                       : fn::combine_narrow_kernel<fn::Bf16>);
+  fn::CombineKernel kern =
+      !wide   ? (f16 ? fn::combine_narrow_kernel<fn::F16> : fn::combine_narrow_kernel<fn::Bf16>)
+      : k > 2 ? (f16 ? fn::combine_kernel<fn::F16, 4> : fn::combine_kernel<fn::Bf16, 4>)
+              : (f16 ? fn::combine_kernel<fn::F16, 2> : fn::combine_kernel<fn::Bf16, 2>);
   const int st = launch(kern, grid, threads, 0, stream, 1, tl_pdl != 0, p);
   if (st == FN_OK)
     record(wide ? MX_VARIANT_COMBINE : MX_VARIANT_COMBINE_NARROW, grid, threads, 1, 1);
