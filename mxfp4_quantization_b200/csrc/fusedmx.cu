@@ -280,7 +280,7 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
     const int64_t fit = p.tok == 16 ? 2 * kSms : kSms;
     while (p.split < 8 && tiles * p.split * 2 <= fit && p.split * 4 <= steps) p.split *= 2;
   }
-  if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * kts > kMaxRows / 8 ||
+  if (p.feat * p.pieces > INT32_MAX / 16 || p.pieces * kts > kMaxRows / 2 ||
       (grouped ? E : 1) * ceil_div(N, 128) * kts > kMaxRows || ceil_div(M, 128) * kts > kMaxRows)
     return FN_ERR_UNSUPPORTED;
   *out = p;
@@ -354,7 +354,7 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   p.box = fn::kMgPairRows / 6;
   if (!code_map(&maps.x, a.codes ? static_cast<const void*>(a.codes) : q.a_q,
                 a.codes ? q.M : q.a_rows, q.K, p.box) ||
-      !scale_map(&maps.xs, a.x_tiles, plan.x_bytes / 512, 16) ||
+      !scale_map(&maps.xs, a.x_tiles, plan.x_bytes / 512, 4) ||
       !scale_map(&maps.ws, a.w_tiles ? a.w_tiles : q.b_scale, tiles_w))
     return FN_ERR_CUDA;
   const int64_t items = std::max(plan.pieces * 2, a.w_tiles ? p.E * ceil_div(q.N, 128) : 0) *

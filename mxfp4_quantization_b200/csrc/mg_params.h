@@ -48,11 +48,11 @@ constexpr int kMgPairFeat = 256;     // features of a pair's tile
 constexpr int kMgPairRows = 240;     // rows of a pair's tile, at most
 constexpr int kMgPairThreads = 384;  // 4 role warps, 8 epilogue warps
 
-constexpr int kMgXTile = 4096;       // a row tile's scales of 128 elements: 2 x 4 copies of 512
+constexpr int kMgXTile = 1024;       // a row tile's scales of 128 elements, 512 bytes per 128 rows
 
 // What the arranging kernel prepares for the pair kernel, in the workspace.
 struct MGArrange {
-  uint8_t* x_tiles;         // [pieces][groups / 4][2 x 128 rows][4 copies] 512-byte tiles
+  uint8_t* x_tiles;         // [pieces][groups / 4][2 x 128 rows] 512-byte tiles
   uint8_t* w_tiles;         // [E][N / 128][groups / 4] tiles of the weights', or nullptr
   uint4* codes;             // [M, K / 32] gathered codes, or nullptr
   const uint4* x_codes;

@@ -20,11 +20,13 @@
 // row-major scales inside the product cost 60 us of 320 (8192 x 8192 x 7168):
 // their tiles pass a fence and a release to the other block in every K step.
 //
-// The rows' scales are written four times, once per group of 32 TMEM lanes, and go
-// to TMEM with two 128-row copies a K step; MMAs wait for the copies in front of
-// them.  With four repeating copies (32 rows each) instead, 8192 x 8192 x 7168 took
-// 275 us against 245, without any copy (wrong sums) 230.  Warps that store the
-// words to TMEM (tcgen05.st) take 1.05 us a K step: 474 us.
+// What bounds it: 8192 x 8192 x 7168 takes 170 us (5660 TFLOP/s; the arranging
+// kernel's 6 us in front included), tensor pipe 77 % busy, L2 to shared memory 15 TB/s,
+// at the power limit when calls follow each other (215 us).  The scale copies, in
+// order with the MMAs, cost the rest of a K step.  Measured and not kept: copies a K
+// step ahead into a second buffer; scales stored four times and copied 128 rows at
+// a time (same time); warps that store the words to TMEM (tcgen05.st: 474 us);
+// heights of 208 and 192 rows (184 us); rows' codes in one box instead of three.
 //
 //   warp 0       TMA
 //   warp 1       one thread of the first block: scale copies and MMAs
@@ -41,7 +43,7 @@ struct MGPShape {
   static constexpr int kSwBytes = 2 * 512;
   static constexpr int kSxBytes = 2 * kMgXTile;
   static constexpr int kStage = kWBytes + kXBytes + kSwBytes + kSxBytes;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 6;
   static constexpr int kColSw = 2 * kMgPairRows;
   static constexpr int kColSx = kColSw + 8;
   static constexpr int kCols = 512;
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
           if (rank == 0) mbar_expect_tx(full + 8 * s, bytes);
           tma_load<2>(w_tile(s), &maps.w, kb * 128, t.e * p.N + f0, bar);
           tma_load<2>(sw_tile(s), &maps.ws, 0, ws0 + 2 * kb, bar);
-          tma_load<2>(sx_tile(s), &maps.xs, 0, (xs0 + 2 * kb) * 8, bar);
+          tma_load<2>(sx_tile(s), &maps.xs, 0, (xs0 + 2 * kb) * 2, bar);
           for (int i = 0; i < pieces; ++i)
             tma_load<2>(x_tile(s) + i * p.box * 128, &maps.x, kb * 128, x0 + i * p.box, bar);
         }
@@ -223,12 +225,14 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
           tc_fence_after();
           const int mmas = min(4, (p.K - kb * kMgStageK + 63) / 64);
           const uint64_t a = operand_desc(w_tile(s)), b = operand_desc(x_tile(s));
-          const uint64_t sw = scale_desc(sw_tile(s)), sx = scale_desc(sx_tile(s), kMgXTile / 2);
+          const uint64_t sw = scale_desc(sw_tile(s)), sx = scale_desc(sx_tile(s));
           if (leader) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               tc_copy_scales<2>(tmem + S::kColSw + 4 * h, sw + 32 * h);
-              tc_copy_rows<2>(tmem + S::kColSx + 8 * h, sx + kMgXTile / 16 * h);
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                tc_copy_scales<2>(tmem + S::kColSx + 4 * (2 * h + b), sx + 32 * (2 * h + b));
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -301,14 +305,13 @@ __global__ void __launch_bounds__(256)
   const int64_t warps = (int64_t)gridDim.x * 8;
   const int64_t first = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
 
-  // the words of tiles 4 c ... 4 c + 3, `step` bytes apart, `copies` times each
-  auto put = [&](uint8_t* tile, int64_t step, int copies, const uint4 (&v)[4], int c) {
+  // the words of tiles 4 c ... 4 c + 3, `step` bytes apart
+  auto put = [&](uint8_t* tile, int64_t step, const uint4 (&v)[4], int c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      for (int k = 0; k < copies; ++k)
-        if (4 * c + i < kts)
-          reinterpret_cast<uint4*>(tile + (4 * c + i) * step + k * 512)[lane] =
-              make_uint4(word(v[0], i), word(v[1], i), word(v[2], i), word(v[3], i));
+      if (4 * c + i < kts)
+        reinterpret_cast<uint4*>(tile + (4 * c + i) * step)[lane] =
+            make_uint4(word(v[0], i), word(v[1], i), word(v[2], i), word(v[3], i));
   };
   int e = 0;
   for (int64_t w = first; w < (int64_t)pieces * 2 * chunks; w += warps) {
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(256)
              : a.x_swizzled ? mg_tiled_scales(p.x_scale, r, c, p.groups)
                             : mg_scales(p.x_scale + (int64_t)r * p.groups, c, p.groups, p.x_wide);
     }
-    put(a.x_tiles + (int64_t)piece * kts * kMgXTile + blk * (kMgXTile / 2), kMgXTile, 4, v, c);
+    put(a.x_tiles + (int64_t)piece * kts * kMgXTile + blk * (kMgXTile / 2), kMgXTile, v, c);
   }
   if (a.w_tiles) {
     const int blocks = (p.N + 127) / 128;
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(256)
                : a.w_swizzled ? mg_tiled_scales(base, r, c, p.groups)
                               : mg_scales(base + r * p.groups, c, p.groups, p.w_wide);
       }
-      put(a.w_tiles + (ex * blocks + b) * kts * 512, 512, 1, v, c);
+      put(a.w_tiles + (ex * blocks + b) * kts * 512, 512, v, c);
     }
   }
   if (a.codes) {  // rows by index; an index outside the operand gives zeros

@@ -262,17 +262,6 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
                  : "memory");
 }
 
-// 128 rows x 32 bytes to eight TMEM columns of all 128 lanes.  On scale tiles that
-// are there four times (once per group of 32 lanes) it does the work of two
-// repeating copies in two thirds of the time of one.
-template <int CG>
-__device__ __forceinline__ void tc_copy_rows(uint32_t taddr, uint64_t desc) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::2.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
 // D[128 CG, N] (+)= A[128 CG, 64] B[N, 64]^T with the E8M0 scales of both operands.
 template <int CG>
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -335,11 +324,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Shared-memory descriptor of scale tiles (16-byte rows, not swizzled, 8-row groups
-// 128 bytes apart; `next`: bytes from a row's first 16 bytes to its second).
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr, uint32_t next = 16) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(next >> 4) << 16 |
-         (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+// Shared-memory descriptor of a 512-byte scale tile (16-byte rows, not swizzled, 8-row
+// groups 128 bytes apart); the next tile's is 32 more.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 |
+         (uint64_t)1 << 46;
 }
 
 }  // namespace fn
