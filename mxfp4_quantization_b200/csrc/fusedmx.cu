@@ -329,6 +329,7 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
     return FN_ERR_CUDA;
   if (!plan.pair) {
     p.box = q.rows ? 1 : plan.tok;
+    p.prefetch = tl_pdl && !grouped ? 1 : 0;  // (an expert's rows are not known before the wait)
     if (!code_map(&maps.x, q.a_q, q.a_rows, q.K, p.box) ||
         (p.x_mode != fn::MG_SCALE_WARP && !scale_map(&maps.xs, q.a_scale, tiles_x)) ||
         (p.w_mode != fn::MG_SCALE_WARP && !scale_map(&maps.ws, q.b_scale, tiles_w)))

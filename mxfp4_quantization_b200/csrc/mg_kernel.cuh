@@ -144,6 +144,16 @@ __global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
     fence_async_smem();
   }
   if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), S::kCols);
+  if (p.prefetch && warp == 0) {
+    // A programmatic dependent: this block's first weights start towards L2 while the
+    // kernel before is still at work (a hint: what that kernel writes is seen all
+    // the same).
+    const int tile = blockIdx.x >> p.split_log2, part = blockIdx.x & (p.split - 1);
+    const int f0 = tile / p.pieces * kMgFeat, steps = (p.K + kMgStageK - 1) / kMgStageK;
+    const int first = steps * part >> p.split_log2, end = steps * (part + 1) >> p.split_log2;
+    const int kb = first + lane;
+    if (kb < min(end, first + S::kStages) && f0 < p.N) tma_prefetch(&maps.w, kb * 128, f0);
+  }
   pdl_enter();
   if (p.offsets && warp == 0) mg_table(p, table, lane, TOK, (p.N + kMgFeat - 1) / kMgFeat, p.pieces);
   if (warp == 0) {

@@ -41,6 +41,7 @@ struct MGParams {
   int box;                  // rows of a token TMA box (1: gather)
   int pieces;               // row tiles there can be, over all experts
   int split, split_log2;    // blocks (a cluster) that share a tile's K steps: 1, 2, 4 or 8
+  int prefetch;             // single blocks: weights towards L2 before the launch wait
   int w_tiles;              // 512-byte scale tiles of one expert's weights
 };
 

@@ -156,6 +156,13 @@ __device__ __forceinline__ void tma_prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Starts a 2-D tile towards L2.
+__device__ __forceinline__ void tma_prefetch(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x),
+               "r"(y)
+               : "memory");
+}
+
 // 2-D tile at (x, y): x in elements of the innermost dimension (16-byte steps), y
 // the row.  CG == 2: `bar` is the mapped address of the pair's first block's barrier.
 template <int CG>
