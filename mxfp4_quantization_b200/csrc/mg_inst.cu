@@ -6,7 +6,7 @@ namespace fn {
 
 template <int TOK, int ID>
 MGInstance instance() {
-  return {mg_kernel<TOK>, TOK, MGShape<TOK>::kSmem, MGShape<TOK>::kPerSm, ID};
+  return {mg_kernel<TOK>, TOK, MGShape<TOK>::kSmem, 2, ID};
 }
 
 MGInstance mg_pick(int tok) {

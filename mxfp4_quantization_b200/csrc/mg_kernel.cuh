@@ -36,9 +36,8 @@ struct MGShape {
   static constexpr int kXBytes = TOK * 128;
   static constexpr int kScaleBytes = 2 * 512;  // of either operand
   static constexpr int kStage = kWBytes + kXBytes + 2 * kScaleBytes;
-  // two blocks fit an SM for the smallest tile
-  static constexpr int kStages = TOK >= 64 ? 8 : 5;
-  static constexpr int kPerSm = TOK >= 64 ? 1 : 2;
+  // two blocks an SM
+  static constexpr int kStages = TOK >= 64 ? 4 : 5;
   // TMEM: two accumulators, then the scales (4 columns per 128 elements each)
   static constexpr int kColSw = 2 * TOK;
   static constexpr int kColSx = kColSw + 8;
@@ -101,7 +100,7 @@ struct MGTiles {
 };
 
 template <int TOK>
-__global__ void __launch_bounds__(kMgThreads, MGShape<TOK>::kPerSm)
+__global__ void __launch_bounds__(kMgThreads, 2)
     mg_kernel(const __grid_constant__ MGParams p, const __grid_constant__ MGMaps maps) {
   using S = MGShape<TOK>;
   extern __shared__ uint8_t dyn[];
