@@ -55,7 +55,7 @@ struct MGPShape {
 // allow, so that no tile is left with a few rows.
 __device__ __forceinline__ int mgp_height(int rows, int tok) {
   const int nt = (rows + tok - 1) / tok;
-  return ((rows + nt - 1) / nt + 15) / 16 * 16;
+  return (rows / nt + (rows % nt != 0) + 15) / 16 * 16;
 }
 
 struct MGPTile {
@@ -359,14 +359,24 @@ __global__ void __launch_bounds__(256)
   }
   if (a.codes) {  // rows by index; an index outside the operand gives zeros
     const int vecs = p.groups;  // 16 bytes hold 32 codes
-    const int64_t total = (int64_t)p.M * vecs;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-      const int64_t r = i / vecs;
+    // a warp a row, or, for short rows, neighbouring lanes a row
+    const int per = vecs >= 32 ? 32 : vecs >= 8 ? 8 : 1, mine = lane % per;
+    const int64_t step = warps * (32 / per);
+    for (int64_t r = first * (32 / per) + lane / per; r < p.M; r += step) {
       const int src = p.rows[r];
-      a.codes[i] = (unsigned)src < (unsigned)p.x_rows
-                       ? ld_stream_nc(a.x_codes + (int64_t)src * vecs + (i - r * vecs))
-                       : make_uint4(0, 0, 0, 0);
+      const bool in = (unsigned)src < (unsigned)p.x_rows;
+      const uint4* from = a.x_codes + (in ? (int64_t)src * vecs : 0);
+      uint4* to = a.codes + r * vecs;
+      for (int v0 = mine; v0 < vecs; v0 += 4 * per) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (v0 + i * per < vecs)
+            x[i] = in ? ld_stream_nc(from + v0 + i * per) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (v0 + i * per < vecs) to[v0 + i * per] = x[i];
+      }
     }
   }
 }

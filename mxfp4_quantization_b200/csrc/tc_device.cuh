@@ -85,21 +85,24 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Every wait ends: after kWaitTries attempts (each of them suspends the thread
-// for a hardware-chosen time first), or as soon as another role of the block
-// has given up, the wait returns false and `stop` is set.  The roles then leave
+// Every wait ends: after kWaitTries attempts (each of them suspends the thread for
+// a hardware-chosen time first), or as soon as another role of the block has
+// given up, the wait returns false and `stop` is set.  The roles then leave
 // their loops and the outputs that are still due are written as NaN.  On
-// working hardware every wait is answered within microseconds.
+// working hardware every wait is answered within microseconds.  All lanes of
+// a warp wait together and get the same answer.
 constexpr int kWaitTries = 1 << 20;
 
 template <int CG>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
+  bool ok = false;
   for (int i = 0; i < kWaitTries; ++i) {
-    if (mbar_try<CG>(bar, parity)) return true;
-    if ((i & 63) == 63 && *stop != 0) return false;
+    ok = mbar_try<CG>(bar, parity);
+    if (ok || ((i & 63) == 63 && *stop != 0)) break;
   }
-  *stop = 1;
-  return false;
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *stop = 1;
+  return ok;
 }
 
 // ---- clusters -----------------------------------------------------------------------------
