@@ -254,15 +254,14 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
   p.pair = each > (grouped ? MX_SMALL_EXPERT_ROWS : MX_SMALL_ROWS);
   if (p.pair) {
     p.feat = ceil_div(N, fn::kMgPairFeat);
-    p.tok = fn::kMgPairRows;
-    if (!grouped) {
-      // the tile height with the least rows times waves of pairs; a tile also costs
-      // about as much as 32 more rows (its weights, its epilogue)
-      int64_t best = INT64_MAX;
-      for (int tok = fn::kMgPairRows; tok >= 48; tok -= 16) {
-        const int64_t cost = ceil_div(ceil_div(M, tok) * p.feat, kSms / 2) * (tok + 32);
-        if (cost < best) best = cost, p.tok = tok;
-      }
+    // the tile height with the least rows times waves of pairs, as if the rows were
+    // spread evenly over the experts; a tile also costs about as much as 32 more
+    // rows (its weights, its epilogue)
+    int64_t best = INT64_MAX;
+    for (int tok = fn::kMgPairRows; tok >= 48; tok -= 16) {
+      const int64_t nt = ceil_div(each, tok), rows = ceil_div(ceil_div(each, nt), 16) * 16;
+      const int64_t waves = ceil_div(nt * (grouped ? E : 1) * p.feat, kSms / 2);
+      if (waves * (rows + 32) < best) best = waves * (rows + 32), p.tok = tok;
     }
     p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
     p.x_bytes = p.pieces * kts * fn::kMgXTile;
