@@ -16,6 +16,7 @@ There is no fallback: if the library is missing, importing this module fails.
 import ctypes
 import os
 from collections import namedtuple
+from functools import lru_cache
 from typing import Optional, Union
 
 import torch
@@ -171,21 +172,21 @@ class programmatic_launch:
 SiluMulQuantOutput = namedtuple("SiluMulQuantOutput", "q scale y")
 
 
-# A decode step makes these calls every few microseconds, so the checks below read
-# each attribute of a tensor once and build nothing they do not need.
+# A decode step makes these calls every few microseconds.  Each first tests what
+# every good call has in one expression (dtype, device number, contiguity: what is
+# cheapest to read); only where that fails the checks that name the fault run.
 
-_U8, _I32 = torch.uint8, torch.int32
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(func, device, *args) -> int:
-    """func(*args, stream) on the current stream of `device`, with that device
-    current."""
-    i = device.index
+def _call(func, i: int, *args) -> int:
+    """func(*args, stream) on the current stream of device number i, with that
+    device current."""
     if i == _current_device():
         return func(*args, _raw_stream(i))
-    with torch.cuda.device(device):
+    with torch.cuda.device(i):
         return func(*args, _raw_stream(i))
 
 
@@ -212,28 +213,32 @@ def _tensor(t: torch.Tensor, name: str, dtype, dim=None, device=None) -> torch.T
     return t
 
 
-def _scale(t: torch.Tensor, name: str, lead: int, rows: int, G: int, device) -> bool:
-    """Checks E8M0 scales of `rows` rows of G groups (per expert, if lead is the
-    number of experts and not 0); True if they are in the 32x4x4 tiling (flat
-    per expert)."""
+def _scale_fault(t: torch.Tensor, name: str, lead: int, rows: int, G: int, device):
+    """Raises for scales that are neither [rows, G] nor the 32x4x4 tiling (per
+    expert, if lead is the number of experts and not 0)."""
     if t.dtype is not _U8 and t.dtype is not torch.float8_e8m0fnu:
         raise TypeError(f"{name} must be uint8 (E8M0 bytes), got {t.dtype}")
     if not t.is_cuda or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    shape = t.shape
-    if lead:
-        if shape[0] == lead:
-            shape = shape[1:]
-        else:
-            shape = ()
-    if len(shape) == 2:
-        if shape[0] == rows and shape[1] == G:
-            return False
-    elif len(shape) == 1 and shape[0] == _round_up(rows, 128) * _round_up(G, 4):
-        return True
     first = f"{lead}, " if lead else ""
     raise ValueError(f"{name} has shape {tuple(t.shape)}: expected ({first}{rows}, {G}), or "
                      f"({first}{_round_up(rows, 128) * _round_up(G, 4)}) in the 32x4x4 tiling")
+
+
+def _tiled(t: torch.Tensor, name: str, lead: int, rows: int, G: int, i: int, device) -> bool:
+    """Whether E8M0 scales of `rows` rows of G groups are in the 32x4x4 tiling (flat
+    per expert) or row-major; raises where they are neither."""
+    if (t.dtype is _U8 or t.dtype is torch.float8_e8m0fnu) and t.get_device() == i and \
+            t.is_contiguous():
+        shape = t.shape
+        n = len(shape) - (1 if lead else 0)
+        if (not lead or shape[0] == lead) and shape[-1] == (G if n == 2 else
+                                                            _round_up(rows, 128) * _round_up(G, 4)):
+            if n == 1:
+                return True
+            if n == 2 and shape[-2] == rows:
+                return False
+    _scale_fault(t, name, lead, rows, G, device)
 
 
 def _product_out(out, out_dtype, M: int, N: int, device):
@@ -242,13 +247,14 @@ def _product_out(out, out_dtype, M: int, N: int, device):
         flag = OUT_FLAGS.get(out_dtype)
         if flag is None:
             raise TypeError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-        return torch.empty((M, N), dtype=out_dtype, device=device), flag, N
-    if not out.is_cuda or out.device != device:
+        # (the quickest of torch's allocating calls)
+        return torch.empty_strided((M, N), (N, 1), dtype=out_dtype, device=device), flag, N
+    if out.device != device:
         raise ValueError(f"out must be on {device}")
     flag = OUT_FLAGS.get(out.dtype)
     if flag is None:
         raise TypeError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
-    if out.dim() != 2 or out.shape[0] != M or out.shape[1] != N:
+    if out.shape != (M, N):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, N)}")
     ldo, step = out.stride()
     if M <= 1:
@@ -258,13 +264,18 @@ def _product_out(out, out_dtype, M: int, N: int, device):
     return out, flag, ldo
 
 
+# (sizes and flags only; a few hundred different ones in a program)
+_gemm_bytes = lru_cache(maxsize=1024)(lambda *a: _lib.mx_gemm_workspace_bytes(*a))
+_grouped_bytes = lru_cache(maxsize=1024)(lambda *a: _lib.mx_grouped_gemm_workspace_bytes(*a))
+
+
 def _workspace(need: int, given: Optional[torch.Tensor], device):
     """The call's workspace: `given`, or one from torch's allocator."""
     if need <= 0:
         return None
     if given is None:
-        return torch.empty((need,), dtype=_U8, device=device)
-    if not given.is_cuda or given.device != device or not given.is_contiguous():
+        return torch.empty_strided((need,), (1,), dtype=_U8, device=device)
+    if given.device != device or not given.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if given.numel() * given.element_size() < need:
         raise ValueError(f"workspace holds fewer than the {need} bytes the call needs")
@@ -279,22 +290,26 @@ def gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: t
     (row-major or in the 32x4x4 tiling).  `out` may have any row stride; its
     type, else `out_dtype`, is the output type (bfloat16, float16, float32).  The
     workspace (mx_gemm_workspace_bytes) is allocated with torch unless given."""
-    dev = a_q.device
-    _tensor(a_q, "a_q", _U8, 2)
-    _tensor(b_q, "b_q", _U8, 2, dev)
+    i = a_q.get_device()
+    if i < 0 or a_q.dtype is not _U8 or b_q.dtype is not _U8 or b_q.get_device() != i or \
+            a_q.dim() != 2 or b_q.dim() != 2 or not a_q.is_contiguous() or \
+            not b_q.is_contiguous():
+        _tensor(a_q, "a_q", _U8, 2)
+        _tensor(b_q, "b_q", _U8, 2, a_q.device)
     M, half = a_q.shape
     N, other = b_q.shape
     if half != other:
         raise ValueError(f"a_q rows have {2 * half} codes, b_q rows {2 * other}")
-    flags = MX_A_SCALE_SWIZZLE if _scale(a_scale, "a_scale", 0, M, half // 16, dev) else 0
-    if _scale(b_scale, "b_scale", 0, N, half // 16, dev):
+    dev = a_q.device
+    flags = MX_A_SCALE_SWIZZLE if _tiled(a_scale, "a_scale", 0, M, half // 16, i, dev) else 0
+    if _tiled(b_scale, "b_scale", 0, N, half // 16, i, dev):
         flags |= MX_B_SCALE_SWIZZLE
     out, f, ldo = _product_out(out, out_dtype, M, N, dev)
     flags |= f
     ws = None
     if M > MX_SMALL_ROWS:
-        ws = _workspace(mx_gemm_workspace_bytes(M, N, 2 * half, flags), workspace, dev)
-    st = _call(_lib.mx_gemm, dev, a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(),
+        ws = _workspace(_gemm_bytes(M, N, 2 * half, flags), workspace, dev)
+    st = _call(_lib.mx_gemm, i, a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(),
                b_scale.data_ptr(), M, N, 2 * half, flags, out.data_ptr(), ldo, _ptr(ws))
     if st != FN_OK:
         raise FusedMXError("mx_gemm", st)
@@ -312,19 +327,24 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     from the rows `rows[r]` (int32 [R]) of a, or from row r itself.  out has
     as many rows as `rows`, else as a_q (an out that is given may have fewer);
     rows that no expert owns keep what they held (a new out is not filled)."""
-    dev = a_q.device
-    _tensor(a_q, "a_q", _U8, 2)
-    _tensor(b_q, "b_q", _U8, 3, dev)
-    _tensor(offsets, "offsets", _I32, 1, dev)
+    i = a_q.get_device()
+    if i < 0 or a_q.dtype is not _U8 or b_q.dtype is not _U8 or offsets.dtype is not _I32 or \
+            b_q.get_device() != i or offsets.get_device() != i or a_q.dim() != 2 or \
+            b_q.dim() != 3 or offsets.dim() != 1 or not a_q.is_contiguous() or \
+            not b_q.is_contiguous() or not offsets.is_contiguous():
+        _tensor(a_q, "a_q", _U8, 2)
+        _tensor(b_q, "b_q", _U8, 3, a_q.device)
+        _tensor(offsets, "offsets", _I32, 1, a_q.device)
     a_rows, half = a_q.shape
     E, N, other = b_q.shape
     if half != other:
         raise ValueError(f"a_q rows have {2 * half} codes, b_q rows {2 * other}")
     if offsets.shape[0] != E + 1:
         raise ValueError(f"offsets has {offsets.shape[0]} entries, expected {E + 1}")
-    if _scale(a_scale, "a_scale", 0, a_rows, half // 16, dev):
+    dev = a_q.device
+    if _tiled(a_scale, "a_scale", 0, a_rows, half // 16, i, dev):
         raise ValueError("a_scale must be row-major [rows, K/32] for ragged row ranges")
-    flags = MX_B_SCALE_SWIZZLE if _scale(b_scale, "b_scale", E, N, half // 16, dev) else 0
+    flags = MX_B_SCALE_SWIZZLE if _tiled(b_scale, "b_scale", E, N, half // 16, i, dev) else 0
     if rows is not None:
         R = _tensor(rows, "rows", _I32, 1, dev).shape[0]
     else:
@@ -333,9 +353,9 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     flags |= f
     ws = None
     if R > MX_SMALL_EXPERT_ROWS * E:
-        ws = _workspace(mx_grouped_gemm_workspace_bytes(R, E, N, 2 * half, flags,
-                                                        int(rows is not None)), workspace, dev)
-    st = _call(_lib.mx_grouped_gemm, dev, a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
+        ws = _workspace(_grouped_bytes(R, E, N, 2 * half, flags, 0 if rows is None else 1),
+                        workspace, dev)
+    st = _call(_lib.mx_grouped_gemm, i, a_q.data_ptr(), a_scale.data_ptr(), a_rows, _ptr(rows),
                offsets.data_ptr(), E, b_q.data_ptr(), b_scale.data_ptr(), R, N, 2 * half, flags,
                out.data_ptr(), ldo, _ptr(ws))
     if st != FN_OK:
@@ -389,7 +409,7 @@ def silu_mul_quant(x: torch.Tensor, mode: Union[int, str], *,
     elif out_y is not None:
         if _tensor(out_y, "out_y", x.dtype, None, dev).numel() != M * H:
             raise ValueError(f"out_y must hold {M} x {H} values")
-    st = _call(_lib.mx_silu_mul_quant, dev, x.data_ptr(), ldx, m, M, H, _ptr(num_rows),
+    st = _call(_lib.mx_silu_mul_quant, dev.index, x.data_ptr(), ldx, m, M, H, _ptr(num_rows),
                out_q.data_ptr(), out_scale.data_ptr(), _ptr(out_y))
     if st != FN_OK:
         raise FusedMXError("mx_silu_mul_quant", st)
@@ -420,24 +440,26 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, *,
     """out[t] = base[t] + sum_j weight[t, j] y[pos[t, j]]: y bf16 (or float16)
     [R, N], pos int32 [T, k] (positions outside [0, R) are skipped), weight
     fp32 [T, k], base and out of y's type [T, N] (out may be base)."""
-    dt = y.dtype
+    dt, i = y.dtype, y.get_device()
     if dt is not torch.bfloat16 and dt is not torch.float16:
         raise TypeError(f"y must be bfloat16 or float16, got {dt}")
-    _tensor(y, "y", dt, 2)
-    dev = y.device
-    _tensor(pos, "pos", _I32, 2, dev)
-    _tensor(weight, "weight", torch.float32, 2, dev)
+    if i < 0 or pos.dtype is not _I32 or weight.dtype is not _F32 or pos.get_device() != i or \
+            weight.get_device() != i or y.dim() != 2 or pos.dim() != 2 or \
+            not y.is_contiguous() or not pos.is_contiguous() or not weight.is_contiguous():
+        _tensor(y, "y", dt, 2)
+        _tensor(pos, "pos", _I32, 2, y.device)
+        _tensor(weight, "weight", _F32, 2, y.device)
     R, N = y.shape
     T, k = pos.shape
     if weight.shape != pos.shape:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, pos {tuple(pos.shape)}")
-    if base is not None and _tensor(base, "base", dt, 2, dev).shape != (T, N):
+    if base is not None and _tensor(base, "base", dt, 2, y.device).shape != (T, N):
         raise ValueError(f"base has shape {tuple(base.shape)}, expected {(T, N)}")
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=dev)
-    elif _tensor(out, "out", dt, 2, dev).shape != (T, N):
+        out = torch.empty_strided((T, N), (N, 1), dtype=dt, device=y.device)
+    elif _tensor(out, "out", dt, 2, y.device).shape != (T, N):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, N)}")
-    st = _call(_lib.mx_combine, dev, y.data_ptr(), R, pos.data_ptr(), weight.data_ptr(),
+    st = _call(_lib.mx_combine, i, y.data_ptr(), R, pos.data_ptr(), weight.data_ptr(),
                _ptr(base), T, k, N, FN_IO_FP16 if dt is torch.float16 else 0, out.data_ptr())
     if st != FN_OK:
         raise FusedMXError("mx_combine", st)
