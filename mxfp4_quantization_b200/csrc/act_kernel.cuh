@@ -116,14 +116,14 @@ __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   constexpr float kLog2e = 1.44269504088896340736f;
   constexpr float kLog2eLo = 1.92596299112661746887e-8f;  // log2(e) - kLog2e
   constexpr float kLn2 = 0.693147180559945309417f;
-  const float2 c = make_float2(-kLog2e, -kLog2e);
-  const float2 t = mul_f32x2(g, c);
-  float2 lo = fma_f32x2(g, c, make_float2(-t.x, -t.y));
-  lo = fma_f32x2(g, make_float2(-kLog2eLo, -kLog2eLo), lo);
+  // t = -g log2(e), lo what t lacks, with the other sign (no negations)
+  const float2 t = mul_f32x2(g, make_float2(-kLog2e, -kLog2e));
+  float2 lo = fma_f32x2(g, make_float2(kLog2e, kLog2e), t);
+  lo = fma_f32x2(g, make_float2(kLog2eLo, kLog2eLo), lo);
   float2 e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  e = fma_f32x2(e, mul_f32x2(lo, make_float2(kLn2, kLn2)), e);
+  e = fma_f32x2(e, mul_f32x2(lo, make_float2(-kLn2, -kLn2)), e);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
   return mul_f32x2(mul_f32x2(g, r), u);  // g u alone can overflow where the result does not
