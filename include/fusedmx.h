@@ -105,9 +105,9 @@ FN_API int64_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int flag
  * rows     int32 [R] or NULL (then a_rows >= R).  A row whose index is outside
  *          [0, a_rows) gives a row of zeros.  An index may occur any number
  *          of times.
- * offsets  int32 [E + 1], non-decreasing, in [0, R].  Other values break the
- *          contract: the rows of out then hold unspecified values, and no
- *          other memory is touched.
+ * offsets  int32 [E + 1], non-decreasing, >= 0; values above R count as R.
+ *          Others break the contract: the rows of out then hold unspecified
+ *          values, and no other memory is touched.
  * b_q      u8 [E, N, K/2];  b_scale [E, N, K/32], or swizzled: E tilings of
  *          roundup(N,128) * roundup(K/32,4) bytes, one after another.
  * R        rows of out, >= 0.  E: 1..MX_MAX_EXPERTS (above: FN_ERR_UNSUPPORTED).

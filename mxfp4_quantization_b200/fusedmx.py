@@ -232,12 +232,13 @@ def _tiled(t: torch.Tensor, name: str, lead: int, rows: int, G: int, i: int, dev
             t.is_contiguous():
         shape = t.shape
         n = len(shape) - (1 if lead else 0)
-        if (not lead or shape[0] == lead) and shape[-1] == (G if n == 2 else
-                                                            _round_up(rows, 128) * _round_up(G, 4)):
-            if n == 1:
-                return True
-            if n == 2 and shape[-2] == rows:
+        if n == 2:
+            if shape[-1] == G and shape[-2] == rows and (not lead or shape[0] == lead):
                 return False
+        elif n == 1:
+            if shape[-1] == _round_up(rows, 128) * _round_up(G, 4) and \
+                    (not lead or shape[0] == lead):
+                return True
     _scale_fault(t, name, lead, rows, G, device)
 
 
@@ -325,8 +326,9 @@ def grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor,
     [E, N, K/32] or [E, bytes of one 32x4x4 tiling]; expert e computes the
     rows offsets[e] <= r < offsets[e+1] (int32 [E+1] on the device) of out
     from the rows `rows[r]` (int32 [R]) of a, or from row r itself.  out has
-    as many rows as `rows`, else as a_q (an out that is given may have fewer);
-    rows that no expert owns keep what they held (a new out is not filled)."""
+    as many rows as `rows`, else as a_q (an out that is given may have fewer:
+    the ranges end there); rows that no expert owns keep what they held (a new
+    out is not filled)."""
     i = a_q.get_device()
     if i < 0 or a_q.dtype is not _U8 or b_q.dtype is not _U8 or offsets.dtype is not _I32 or \
             b_q.get_device() != i or offsets.get_device() != i or a_q.dim() != 2 or \

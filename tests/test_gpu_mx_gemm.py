@@ -166,9 +166,20 @@ def test_empty_and_refused_calls(fx):
     g = gpu_util.Guarded((4, 8), BF)
     for args, kind in (((aq, as_.int(), bq, bs), TypeError), ((aq, as_[:3], bq, bs), ValueError),
                        ((aq, as_, bq[:, :16], bs), ValueError), ((aq.cpu(), as_, bq, bs), ValueError),
-                       ((aq.t(), as_, bq, bs), ValueError)):
+                       ((aq.t(), as_, bq, bs), ValueError), ((aq, as_[0, 0], bq, bs), ValueError),
+                       ((aq, as_, bq, bs.cpu()), ValueError), ((aq, as_.view(-1), bq, bs), ValueError),
+                       ((aq, as_, bq.cpu(), bs), ValueError), ((aq.int(), as_, bq, bs), TypeError),
+                       ((aq[None], as_, bq, bs), ValueError), ((aq, as_, bq, bs.t()), ValueError)):
         with pytest.raises(kind):
             fx.gemm(*args, out=g.t)
+    with pytest.raises(ValueError):
+        fx.gemm(aq, as_, bq, bs, out=torch.empty((4, 8), dtype=BF))
+    with pytest.raises(ValueError):  # rows that overlap
+        fx.gemm(aq, as_, bq, bs, out=torch.empty(8, dtype=BF, device="cuda").expand(4, 8))
+    shifted = torch.empty(4 * 32 + 8, dtype=torch.uint8, device="cuda")[8:].view(4, 32)
+    with pytest.raises(fx.FusedMXError) as e:  # codes 8 bytes off
+        fx.gemm(shifted, as_, bq, bs, out=g.t)
+    assert e.value.status == -2
     with pytest.raises(ValueError):
         fx.gemm(aq, as_, bq, bs, out=g.t[:3])
     with pytest.raises(TypeError):

@@ -122,3 +122,30 @@ def test_equals_gemm(fx):
     assert torch.equal(fx.grouped_gemm(aq, as_, bq, bs, off), one)
     every = torch.arange(M, dtype=torch.int32, device="cuda")
     assert torch.equal(fx.grouped_gemm(aq, as_, bq, bs, off, rows=every), one)
+
+
+def test_refused_calls(fx):
+    aq, as_ = mx_ref.codes(6, 64, 1), mx_ref.scales(6, 64, 1)
+    bq, bs, arg = weights(3, 40, 64, 2, True)
+    off = torch.tensor([0, 2, 2, 6], dtype=torch.int32, device="cuda")
+    rows = torch.zeros(6, dtype=torch.int32, device="cuda")
+    g = gpu_util.Guarded((6, 40), BF)
+    for args, kind in (((aq, as_, bq, bs, off[:3]), ValueError), ((aq, as_, bq, bs, off.long()), TypeError),
+                       ((aq, as_, bq[0], bs, off), ValueError), ((aq, as_, bq, bs[:2], off), ValueError),
+                       ((aq, as_, bq, bs[0], off), ValueError), ((aq, as_[:5], bq, bs, off), ValueError),
+                       ((aq, as_, bq, bs, off.cpu()), ValueError),
+                       ((aq, mx_ref.tile(as_), bq, bs, off), ValueError),
+                       ((aq, as_, bq[:, :, :16], bs, off), ValueError)):
+        with pytest.raises(kind):
+            fx.grouped_gemm(*args, out=g.t)
+    for r in (rows.long(), rows.cpu(), rows[::2]):
+        with pytest.raises((TypeError, ValueError)):
+            fx.grouped_gemm(aq, as_, bq, bs, off, rows=r)
+    with pytest.raises(ValueError):  # more rows of out than of a, without an index
+        fx.grouped_gemm(aq, as_, bq, bs, off, out=torch.empty((7, 40), dtype=BF, device="cuda"))
+    torch.cuda.synchronize()
+    assert g.untouched()
+    # fewer rows of out than of a: the owned rows beyond it are left out
+    part = fx.grouped_gemm(aq, as_, bq, bs, off, out=g.t[:4])
+    assert torch.equal(part, fx.grouped_gemm(aq, as_, bq, bs, off)[:4])
+    assert bool((g.t[4:].view(torch.uint8) == gpu_util.CANARY).all())

@@ -1,5 +1,8 @@
 """The calls of libfusedmx.so that ordinary sizes do not reach: offsets past 32 bits,
 threads and streams at once, graphs, a workspace used again and again, zero rows."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -192,3 +195,35 @@ def test_graphs_that_hold_the_pair_kernels(fx):
                 gr.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+FIRST_CALL = """
+import torch
+from tests import mx_ref
+from mxfp4_quantization_b200 import fusedmx as fx
+sets = [(mx_ref.codes(m, 544, m), mx_ref.scales(m, 544, m), mx_ref.codes(200, 544, 1),
+         mx_ref.scales(200, 544, 1)) for m in (3, 40, 300)]
+x = torch.randn((5, 512), device="cuda").to(torch.bfloat16)
+held = [torch.zeros((s[0].shape[0], 200), dtype=torch.bfloat16, device="cuda") for s in sets]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for s, o in zip(sets, held):
+        fx.gemm(*s, out=o)
+    q = fx.silu_mul_quant(x, "mxfp4").q
+graph.replay()
+torch.cuda.synchronize()
+for s, o in zip(sets, held):
+    assert torch.equal(fx.gemm(*s), o)
+assert torch.equal(fx.silu_mul_quant(x, "mxfp4").q, q)
+print("captured first calls: ok")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(fx):
+    """Nothing has to run before a capture: the library's one-time look-ups work
+    inside it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured first calls: ok" in r.stdout, r.stderr[-2000:]
