@@ -310,6 +310,11 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   p.w_wide = p.groups % 16 == 0 && aligned(q.b_scale, 16);
   p.out_type = q.flags & 0xF;
   p.out_quads = p.out_type != MX_OUT_FP32 && q.N % 4 == 0 && q.ldo % 4 == 0 && aligned(q.out, 8);
+  // fp32 rows in 8-byte stores where the epilogue sets the pace, in 4-byte stores where
+  // the MMAs do and its shuffles cost them issue slots: 8192 x 7168, K = 2048
+  // 80 us / 90 us, 8192 x 8192, K = 7168 184 us / 180 us
+  p.out_pairs = p.out_type == MX_OUT_FP32 && q.K <= 4096 && q.N % 2 == 0 && q.ldo % 2 == 0 &&
+                aligned(q.out, 8);
   p.tok = plan.tok;
   p.pieces = (int)plan.pieces;
   p.split = plan.split;

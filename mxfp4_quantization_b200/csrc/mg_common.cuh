@@ -122,6 +122,22 @@ template <int C>
 __device__ __forceinline__ void mg_store(const MGParams& p, uint32_t (&v)[C], int64_t row, int n,
                                          int f, int lane) {
   if (p.out_type == MG_OUT_FP32) {
+    if (p.out_pairs) {  // neighbouring lanes trade rows for pairs of features
+      const int odd = lane & 1, pair = f & ~1;
+      float* o = static_cast<float*>(p.out) + (row + odd) * p.ldo + pair;
+      float2 w[C / 2];
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+        w[i] = odd ? make_float2(__uint_as_float(got), __uint_as_float(v[2 * i + 1]))
+                   : make_float2(__uint_as_float(v[2 * i]), __uint_as_float(got));
+      }
+      const int mine = pair < p.N ? n - odd : 0;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i)
+        if (2 * i < mine) *reinterpret_cast<float2*>(o + 2 * i * p.ldo) = w[i];
+      return;
+    }
     float* o = static_cast<float*>(p.out) + row * p.ldo + f;
 #pragma unroll
     for (int i = 0; i < C; ++i)

@@ -37,6 +37,7 @@ struct MGParams {
   int x_wide, w_wide;       // row-major scale rows are whole aligned 16-byte vectors
   int out_type;
   int out_quads;            // 16-bit output whose rows are whole aligned groups of 4
+  int out_pairs;            // fp32 output in aligned pairs
   int tok;                  // pair kernel: rows of a tile, a multiple of 16
   int box;                  // rows of a token TMA box (1: gather)
   int pieces;               // row tiles there can be, over all experts
