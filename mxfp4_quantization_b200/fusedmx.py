@@ -14,6 +14,7 @@ Scales are told apart by their shape, as fusednorm.alloc_outputs makes them:
 There is no fallback: if the library is missing, importing this module fails.
 """
 import ctypes
+import math
 import os
 from collections import namedtuple
 from functools import lru_cache
@@ -21,7 +22,7 @@ from typing import Optional, Union
 
 import torch
 
-from .fusednorm import (FN_FP8_PER_TOKEN, FN_IO_FP16, FN_MODE_MASK, FN_MXFP4, FN_OK,
+from .fusednorm import (FN_FP8_PER_GROUP128, FN_FP8_PER_TOKEN, FN_IO_FP16, FN_MODE_MASK, FN_MXFP4, FN_OK,
                         FN_SCALE_MN_MAJOR, FN_SCALE_SWIZZLE_32_4_4, MODES, alloc_outputs)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfusedmx.so")
@@ -377,29 +378,32 @@ def silu_mul_quant(x: torch.Tensor, mode: Union[int, str], *,
     (int32 [1] on the device): only the first *num_rows rows are computed."""
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    dt = x.dtype
     m = MODES[mode] if isinstance(mode, str) else int(mode)
-    if x.dtype == torch.float16:
+    if dt is torch.float16:
         m |= FN_IO_FP16
+    elif dt is not torch.bfloat16:
+        raise TypeError(f"x must be bfloat16 or float16, got {dt}")
     elif m & FN_IO_FP16:
         raise TypeError("FN_IO_FP16 was asked for but the rows are bfloat16")
-    if x.shape[-1] % 2:
-        raise ValueError("x rows hold a gate half and an up half: an even last dim")
-    H = x.shape[-1] // 2
     if x.dim() != 2:
-        if not x.is_contiguous():
+        if not x.is_contiguous() or x.dim() == 0:
             raise ValueError("x must be contiguous, or 2-D with a contiguous last dim")
-        x = x.reshape(-1, 2 * H)
-    M = x.shape[0]
-    if x.stride(1) != 1 and x.shape[1] > 1:
+        x = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+    M, H = x.shape
+    if H % 2:
+        raise ValueError("x rows hold a gate half and an up half: an even last dim")
+    ldx, step = x.stride()
+    if step != 1 and H > 1:
         raise ValueError("x needs a contiguous last dim")
-    ldx = x.stride(0) if M > 1 else 2 * H
+    if M <= 1:
+        ldx = H
+    H //= 2
     dev = x.device
     if num_rows is not None and _tensor(num_rows, "num_rows", torch.int32, None, dev).numel() != 1:
         raise ValueError("num_rows must hold one value")
     if out_q is None and out_scale is None:
-        out_q, out_scale = alloc_outputs(m, M, H, dev)
+        out_q, out_scale = _alloc_quant(m, M, H, dev)
     else:
         if out_q is None or out_scale is None:
             q, s = alloc_outputs(m, M, H, dev)
@@ -407,15 +411,30 @@ def silu_mul_quant(x: torch.Tensor, mode: Union[int, str], *,
             out_scale = s if out_scale is None else out_scale
         _check_quant(out_q, out_scale, m, M, H, dev)
     if out_y is None and emit_y:
-        out_y = torch.empty((M, H), dtype=x.dtype, device=dev)
+        out_y = torch.empty_strided((M, H), (H, 1), dtype=dt, device=dev)
     elif out_y is not None:
-        if _tensor(out_y, "out_y", x.dtype, None, dev).numel() != M * H:
+        if _tensor(out_y, "out_y", dt, None, dev).numel() != M * H:
             raise ValueError(f"out_y must hold {M} x {H} values")
     st = _call(_lib.mx_silu_mul_quant, dev.index, x.data_ptr(), ldx, m, M, H, _ptr(num_rows),
                out_q.data_ptr(), out_scale.data_ptr(), _ptr(out_y))
     if st != FN_OK:
         raise FusedMXError("mx_silu_mul_quant", st)
     return SiluMulQuantOutput(out_q, out_scale, out_y)
+
+
+def _alloc_quant(mode: int, M: int, H: int, device):
+    """fusednorm.alloc_outputs, for row-major scales by torch's quickest call."""
+    kind = mode & ~FN_IO_FP16
+    if kind == FN_MXFP4:
+        dt, w, sdt, g = _U8, H // 2, _U8, H // 32
+    elif kind == FN_FP8_PER_TOKEN:
+        dt, w, sdt, g = torch.float8_e4m3fn, H, _F32, 1
+    elif kind == FN_FP8_PER_GROUP128:
+        dt, w, sdt, g = torch.float8_e4m3fn, H, _F32, H // 128
+    else:
+        return alloc_outputs(mode, M, H, device)
+    return (torch.empty_strided((M, w), (w, 1), dtype=dt, device=device),
+            torch.empty_strided((M, g), (g, 1), dtype=sdt, device=device))
 
 
 def _check_quant(q, scale, mode: int, M: int, H: int, device):
