@@ -20,8 +20,8 @@
 // row-major scales inside the product cost 60 us of 320 (8192 x 8192 x 7168):
 // their tiles pass a fence and a release to the other block in every K step.
 //
-// What bounds it: 8192 x 8192 x 7168 takes 170 us (5660 TFLOP/s; the arranging
-// kernel's 6 us in front included), tensor pipe 77 % busy, L2 to shared memory 15 TB/s,
+// What bounds it: 8192 x 8192 x 7168 takes 166-182 us (5300-5800 TFLOP/s; the arranging
+// kernel's 6 us in front included), tensor pipe 77 % busy, L2 to shared memory 13 TB/s,
 // at the power limit when calls follow each other (215 us).  The scale copies, in
 // order with the MMAs, cost the rest of a K step.  Measured and not kept: copies a K
 // step ahead into a second buffer; scales stored four times and copied 128 rows at
