@@ -18,6 +18,10 @@ struct ActParams {
   int nvec;                 // H / 8
   int scale_layout;
   int64_t scale_ld;
+  // ceil(2^64 / nvec) and ceil(2^32 / nvec), nvec >= 4: the high half of their product
+  // with i is i / nvec, exactly, while i (nvec - 1) < 2^64 (2^32)
+  uint64_t recip64;
+  uint32_t recip32;
 };
 
 // The real value's nearest 16-bit neighbour through fp64.  p = g u (and p / 2) is
@@ -124,8 +128,9 @@ __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
   e = fma_f32x2(e, mul_f32x2(lo, make_float2(-kLn2, -kLn2)), e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
+  const float2 d = fma_f32x2(e, make_float2(1.f, 1.f), make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return mul_f32x2(mul_f32x2(g, r), u);  // g u alone can overflow where the result does not
 }
 
@@ -219,8 +224,8 @@ __global__ void __launch_bounds__(256, 6) act_groups_kernel(const ActParams p) {
   const int64_t rows = act_rows(p), total = rows * p.nvec;
   for (int64_t i0 = (int64_t)blockIdx.x * (256 * kActVecs); i0 < total;
        i0 += (int64_t)gridDim.x * (256 * kActVecs)) {
-    // one 64-bit division a block; a vector is then at most 511 past (r0, v0)
-    const int64_t r0 = i0 / p.nvec;
+    // a vector is at most 511 past (r0, v0), v0 < nvec <= 4096
+    const int64_t r0 = (int64_t)__umul64hi((uint64_t)i0, p.recip64);
     const int v0 = (int)(i0 - r0 * p.nvec);
     int64_t row[kActVecs];
     int v[kActVecs];
@@ -229,8 +234,7 @@ __global__ void __launch_bounds__(256, 6) act_groups_kernel(const ActParams p) {
 #pragma unroll
     for (int k = 0; k < kActVecs; ++k) {
       const unsigned at = (unsigned)(v0 + k * 256 + (int)threadIdx.x);
-      const unsigned down = p.nvec >= 256 * kActVecs ? (at >= (unsigned)p.nvec ? 1u : 0u)
-                                                     : at / (unsigned)p.nvec;
+      const unsigned down = __umulhi(at, p.recip32);
       row[k] = r0 + down;
       v[k] = (int)(at - down * (unsigned)p.nvec);
       ok[k] = row[k] < rows;

@@ -550,6 +550,8 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
     if (st == FN_OK) record(MX_VARIANT_SILU_ROW, grid, threads, V, 1);
     return st;
   }
+  p.recip64 = UINT64_MAX / (uint64_t)p.nvec + 1;
+  p.recip32 = UINT32_MAX / (uint32_t)p.nvec + 1;
   // two vectors a thread once every SM has eight blocks of one
   const int vecs = M * p.nvec > (int64_t)sms * 8 * 256 ? 2 : 1;
   const int64_t per = 256 * vecs;
