@@ -18,8 +18,8 @@ struct ActParams {
   int nvec;                 // H / 8
   int scale_layout;
   int64_t scale_ld;
-  // ceil(2^64 / nvec) and ceil(2^32 / nvec), nvec >= 4: the high half of their product
-  // with i is i / nvec, exactly, while i (nvec - 1) < 2^64 (2^32)
+  // ceil(2^64 / n) and ceil(2^32 / n) for the n >= 2 units of a row (group modes): the high
+  // half of their product with i is i / n, exactly, while i (n - 1) < 2^64 (2^32)
   uint64_t recip64;
   uint32_t recip32;
 };
@@ -106,15 +106,17 @@ __device__ __forceinline__ uint32_t silu_mul_mid(float g, float u) {
   return IO::pack(f, 0.f) & 0xFFFFu;
 }
 
-// fp32 value of g u / (1 + e^-g), relative error below kSiluErr where it is used
-// (g >= -87, |result| >= 2^-100).  e^-g = 2^t with t = -g log2(e) in two parts:
+// The lower end of an interval that holds g u / (1 + e^-g); its product with
+// kSiluWidth is the upper one (g >= -87, |result| >= 2^-100).  e^-g = 2^t with t = -g log2(e) in two parts:
 // the rounded product and its remainder, which scales the result by 1 + t_lo ln 2.
 // Errors, in units of 2^-24: ex2.approx 4 (2^-22), the remainder's terms 1, their
 // product 1, the sum 1 + e^-g 1 (and it passes on at most the 6 before), the
-// approximate reciprocal 2, two products 2: 12 in all, below 2^-20.4.  (The .ftz
-// forms: an e^-g below 2^-126 adds nothing to 1, and 1 + e^-g stays below 2^126,
+// approximate reciprocal 2, two products 2: below 12 in all.  The sum comes scaled by
+// 1 + 14 units, so the result is 2 to 26 below the real value, and 28 more, less
+// the rounding of that product, are above it.  (The .ftz forms: an e^-g below 2^-126 adds nothing to 1, and 1 + e^-g stays below 2^126,
 // so neither result that matters is subnormal.)
-constexpr float kSiluErr = 0x1p-20f;
+constexpr float kSiluUp = 1.f + 14 * 0x1p-24f;
+constexpr float kSiluWidth = 1.f + 28 * 0x1p-24f;
 
 __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -128,7 +130,7 @@ __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
   e = fma_f32x2(e, mul_f32x2(lo, make_float2(-kLn2, -kLn2)), e);
-  const float2 d = fma_f32x2(e, make_float2(1.f, 1.f), make_float2(1.f, 1.f));
+  const float2 d = fma_f32x2(e, make_float2(kSiluUp, kSiluUp), make_float2(kSiluUp, kSiluUp));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return mul_f32x2(mul_f32x2(g, r), u);  // g u alone can overflow where the result does not
@@ -141,28 +143,40 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t half_of(const uint4& v, int i) {
-  return word(v, i >> 1) >> (16 * (i & 1)) & 0xFFFFu;
-}
+template <int N>
+struct SiluVecs {
+  uint4 y[N];
+};
 
-// Recomputes the elements of `mask`: every lane its own next one, so lanes that
-// missed different elements share a pass.
-template <class IO>
-__device__ __noinline__ uint4 silu_mul_redo(uint4 g, uint4 u, uint4 y, uint32_t mask) {
+// Recomputes the elements of `mask` (8 bits a vector) of N vectors, their gates at src
+// and every `step` vectors on, their ups nvec vectors behind (read again, 2 bytes each,
+// from L2): every lane its own next one, so lanes that missed different elements share
+// a pass.
+template <class IO, int N>
+__device__ __noinline__ SiluVecs<N> silu_mul_redo(SiluVecs<N> s, const uint4* src, int step,
+                                                  int nvec, uint32_t mask) {
+  const uint16_t* g = reinterpret_cast<const uint16_t*>(src);
   while (mask) {
     const int i = __ffs(mask) - 1, w = i >> 1, sh = 16 * (i & 1);
     mask &= mask - 1;
-    const uint32_t r = silu_mul_mid<IO>(IO::lo(half_of(g, i)), IO::lo(half_of(u, i)));
-    set_word(y, w, (word(y, w) & ~(0xFFFFu << sh)) | r << sh);
+    const uint16_t* at = g + (w >> 2) * step * 8 + (i & 7);
+    const uint32_t r = silu_mul_mid<IO>(IO::lo(__ldg(at)), IO::lo(__ldg(at + nvec * 8)));
+    const uint32_t keep = ~(0xFFFFu << sh);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (w == 4 * k + j) set_word(s.y[k], j, (word(s.y[k], j) & keep) | r << sh);
+    }
   }
-  return y;
+  return s;
 }
 
 // y of 8 elements.  The two ends of the interval that holds the real value
 // round to one 16-bit value unless a midpoint lies between them; one test
-// covers all 8 (bf16: 9 % of warps fail it somewhere, binary16: half).
+// covers all 8.  Returns the mask of the elements that stay open.
 template <class IO>
-__device__ __forceinline__ uint4 silu_mul_vec(const uint4& gv, const uint4& uv) {
+__device__ __forceinline__ uint32_t silu_mul_fast(const uint4& gv, const uint4& uv, uint4& out) {
   uint32_t a[4], y[4], differ = 0;
   float2 v[4];
   float vmin = 1.f;
@@ -171,18 +185,17 @@ __device__ __forceinline__ uint4 silu_mul_vec(const uint4& gv, const uint4& uv) 
     const float2 g = make_float2(IO::lo(word(gv, i)), IO::hi(word(gv, i)));
     const float2 u = make_float2(IO::lo(word(uv, i)), IO::hi(word(uv, i)));
     v[i] = silu_mul_fp32(g, u);
-    const float2 l = mul_f32x2(v[i], make_float2(1.f - kSiluErr, 1.f - kSiluErr));
-    const float2 h = mul_f32x2(v[i], make_float2(1.f + kSiluErr, 1.f + kSiluErr));
-    a[i] = IO::pack(l.x, l.y);
+    const float2 h = mul_f32x2(v[i], make_float2(kSiluWidth, kSiluWidth));
+    a[i] = IO::pack(v[i].x, v[i].y);
     y[i] = IO::pack(h.x, h.y);
     differ |= a[i] ^ y[i];
     vmin = min_nan(vmin, fabsf(v[i].x), fabsf(v[i].y));
   }
-  uint4 out = make_uint4(y[0], y[1], y[2], y[3]);
+  out = make_uint4(y[0], y[1], y[2], y[3]);
+  uint32_t mask = 0;
   // (g below -87.3, where 1 / (1 + e^-g) leaves the normal range, gives 0 here)
   const bool far = !(vmin >= 0x1p-100f);
   if (differ != 0 || far) {
-    uint32_t mask = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = a[i] ^ y[i];
@@ -198,9 +211,27 @@ __device__ __forceinline__ uint4 silu_mul_vec(const uint4& gv, const uint4& uv) 
         if (!(g1 >= -87.f) || !(fabsf(v[i].y) >= 0x1p-100f || v[i].y == 0.f)) mask |= 2u << (2 * i);
       }
     }
-    if (mask) out = silu_mul_redo<IO>(gv, uv, out, mask);
   }
-  return out;
+  return mask;
+}
+
+// y of N vectors, `step` apart from src on; `skip`: the mask of elements not asked for.
+template <class IO, int N>
+__device__ __forceinline__ void silu_mul_vecs(const uint4 (&g)[N], const uint4 (&u)[N], uint4* y,
+                                              const uint4* src, int step, int nvec,
+                                              uint32_t skip = 0) {
+  uint32_t mask = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) mask |= silu_mul_fast<IO>(g[k], u[k], y[k]) << (8 * k);
+  mask &= ~skip;
+  if (mask) {
+    SiluVecs<N> s;
+#pragma unroll
+    for (int k = 0; k < N; ++k) s.y[k] = y[k];
+    s = silu_mul_redo<IO, N>(s, src, step, nvec, mask);
+#pragma unroll
+    for (int k = 0; k < N; ++k) y[k] = s.y[k];
+  }
 }
 
 __device__ __forceinline__ int64_t act_rows(const ActParams& p) {
@@ -209,59 +240,93 @@ __device__ __forceinline__ int64_t act_rows(const ActParams& p) {
   return n < 0 ? 0 : n < p.M ? n : p.M;
 }
 
-// Group modes (MXFP4, FP8 per 128): the rows laid end to end, kActVecs 8-element
-// vectors a thread with all their loads first (two where there is work for
-// it, one for decode-sized calls); groups are 4 or 16 neighbouring lanes.
-// Bound by instructions, 33 an element: two special-function operations, ten packed
-// fp32, the interval test, the quantization.  32768 x 2048: MXFP4 from bf16 78 us
-// (3.9 TB/s), FP8 per 128 89 us; from binary16, whose midpoints lie eight times as
-// close, 99 and 110 us.  With four blocks an SM instead of six 85 us, with
-// four vectors a thread 75 and 89 (binary16 100 and 116).
-template <int MODE, class IO, int kActVecs>
-__global__ void __launch_bounds__(256, 6) act_groups_kernel(const ActParams p) {
+// Group modes (MXFP4, FP8 per 128): the rows laid end to end, N neighbouring 8-element
+// vectors a thread (two where there is work for it, one for decode-sized calls);
+// groups are 4 / N or 16 / N neighbouring lanes.  Bound by instructions: two
+// special-function operations an element, ten packed fp32 a pair, the interval
+// test, the quantization.  32768 x 2048: MXFP4 from bf16 63 us (4.8 TB/s), FP8 per 128
+// 71 us; from binary16, whose midpoints lie eight times as close, 77 and 84 us.
+// With vectors 256 apart instead of neighbours (their own scales and twice the
+// shuffles) and each one's open elements on their own 73, 85, 94 and 106 us; with
+// divisions for the rows 78, 89, 99 and 110.  A thread's 32 bytes in one load take the
+// same time.
+template <int MODE, class IO, int N>
+__global__ void __launch_bounds__(256, IO::kF16 ? 6 : 5) act_groups_kernel(const ActParams p) {
   pdl_enter();
+  constexpr int kLanes = (MODE == MODE_MX ? 4 : 16) / N;
   const int lane = threadIdx.x & 31;
-  const int64_t rows = act_rows(p), total = rows * p.nvec;
-  for (int64_t i0 = (int64_t)blockIdx.x * (256 * kActVecs); i0 < total;
-       i0 += (int64_t)gridDim.x * (256 * kActVecs)) {
-    // a vector is at most 511 past (r0, v0), v0 < nvec <= 4096
-    const int64_t r0 = (int64_t)__umul64hi((uint64_t)i0, p.recip64);
-    const int v0 = (int)(i0 - r0 * p.nvec);
-    int64_t row[kActVecs];
-    int v[kActVecs];
-    bool ok[kActVecs];
-    uint4 g[kActVecs], u[kActVecs];
+  const int units = p.nvec / N;
+  const int64_t rows = act_rows(p), i0 = (int64_t)blockIdx.x * 256;
+  if (i0 >= rows * units) return;
+  // a unit is at most 255 past (r0, v0), v0 < units <= 4096
+  const int64_t r0 = (int64_t)__umul64hi((uint64_t)i0, p.recip64);
+  const unsigned at = (unsigned)(i0 - r0 * units) + threadIdx.x;
+  const unsigned down = __umulhi(at, p.recip32);
+  int64_t row = r0 + down;
+  int v = (int)(at - down * (unsigned)units) * N;
+  const bool ok = row < rows;
+  if (!ok) row = 0, v = 0;
+  uint4 g[N], u[N], y[N];
+  const uint4* src = p.x + row * p.ldv + v;
 #pragma unroll
-    for (int k = 0; k < kActVecs; ++k) {
-      const unsigned at = (unsigned)(v0 + k * 256 + (int)threadIdx.x);
-      const unsigned down = __umulhi(at, p.recip32);
-      row[k] = r0 + down;
-      v[k] = (int)(at - down * (unsigned)p.nvec);
-      ok[k] = row[k] < rows;
-      if (!ok[k]) row[k] = 0, v[k] = 0;
-      const uint4* src = p.x + row[k] * p.ldv + v[k];
-      g[k] = ld_stream_nc(src);
-      u[k] = ld_stream_nc(src + p.nvec);
-    }
+  for (int k = 0; k < N; ++k) {
+    g[k] = ld_stream_nc(src + k);
+    u[k] = ld_stream_nc(src + p.nvec + k);
+  }
+  silu_mul_vecs<IO, N>(g, u, y, src, 1, p.nvec);
 #pragma unroll
-    for (int k = 0; k < kActVecs; ++k) {
-      const uint4 y = silu_mul_vec<IO>(g[k], u[k]);
-      if (p.out_y && ok[k]) st_stream(p.out_y + row[k] * p.nvec + v[k], y);
-      quant_store<MODE, IO>(y, ok[k], lane, row[k], v[k], p.nvec * 8,
-                            Fp8Scale{1.f, 1.f, 0.f, false}, p.out_q, p.out_scale, p.scale_layout,
-                            p.scale_ld);
-    }
+  for (int k = 0; k < N; ++k) {
+    if (p.out_y && ok) st_stream(p.out_y + row * p.nvec + v + k, y[k]);
+  }
+  float a = vec_absmax<IO>(y[0]);
+  if constexpr (MODE == MODE_MX) {
+    if constexpr (N == 2) a = fmaxf(a, vec_absmax<IO>(y[1]));
+    float inv;
+    const uint32_t e8 = mx_scale(group_max<kLanes>(a), inv);
+    uint32_t q[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) q[k] = e2m1_codes<IO>(y[k], inv);
+    if (!ok) return;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out_q + row * (int64_t)(p.nvec * 4)) + v;
+    if constexpr (N == 2)
+      st_stream(reinterpret_cast<uint2*>(dst), make_uint2(q[0], q[1]));
+    else
+      st_stream(dst, q[0]);
+    if (lane % kLanes == 0)
+      static_cast<uint8_t*>(p.out_scale)[scale_index(p.scale_layout, p.scale_ld, row, v / 4,
+                                                     p.nvec / 4)] = (uint8_t)e8;
+  } else {
+    // (as bits: a vector of NaN counts as the largest, as in quant_vec)
+    uint32_t am = __float_as_uint(a);
+    if constexpr (N == 2) am = max(am, __float_as_uint(vec_absmax<IO>(y[1])));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const Fp8Scale s = fp8_scale_direct(__uint_as_float(am));
+    const bool exact = __any_sync(0xffffffffu, s.exact_div);
+    uint2 q[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) q[k] = e4m3_codes_uniform<IO>(y[k], s, exact);
+    if (!ok) return;
+    uint2* dst = reinterpret_cast<uint2*>(p.out_q + row * (int64_t)(p.nvec * 8)) + v;
+    if constexpr (N == 2)
+      st_stream(reinterpret_cast<uint4*>(dst), make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
+    else
+      st_stream(dst, q[0]);
+    if (lane % kLanes == 0)
+      static_cast<float*>(p.out_scale)[scale_index(p.scale_layout, p.scale_ld, row, v / 16,
+                                                   p.nvec / 16)] = s.s;
   }
 }
 
 // Per-token mode: a block per row, the row in registers (V vectors a thread)
-// between the maximum and the codes.  bf16, 67 M elements: 92 us at H = 2048, 69 us
-// (4.8 TB/s) at 8192, 77 us at 16384; the blocks an SM are held to were
-// measured (16384: 87 us at two, 144 us at one).
+// between the maximum and the codes.  bf16, 67 M elements: 65 us at H = 1024 and 2048
+// (5.2 TB/s), 68 us at 8192, 75 us at 16384, 103 us at 32768; the sizes of the blocks,
+// both ways, are at the launch.
 template <int V, class IO>
-__global__ void __launch_bounds__(256, V == 1 ? 8 : V == 2 ? 6 : V == 4 ? 4 : V == 8 ? 3 : 1) act_row_kernel(const ActParams p) {
+__global__ void __launch_bounds__(512, V == 1 ? 4 : V == 2 ? 3 : V == 4 ? 2 : 1)
+    act_row_kernel(const ActParams p) {
   pdl_enter();
-  __shared__ float red[8];
+  __shared__ float red[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
   const int64_t rows = act_rows(p);
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -271,17 +336,20 @@ __global__ void __launch_bounds__(256, V == 1 ? 8 : V == 2 ? 6 : V == 4 ? 4 : V 
 #pragma unroll
     for (int k0 = 0; k0 < V; k0 += B) {
       uint4 g[B], u[B];
+      uint32_t skip = 0;
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         const int v = threadIdx.x + (k0 + k) * blockDim.x;
         const uint4* src = p.x + row * p.ldv + (v < p.nvec ? v : 0);
+        if (v >= p.nvec) skip |= 0xFFu << (8 * k);
         g[k] = ld_stream_nc(src);
         u[k] = ld_stream_nc(src + p.nvec);
       }
+      silu_mul_vecs<IO, B>(g, u, y + k0, p.x + row * p.ldv + threadIdx.x + k0 * blockDim.x,
+                           blockDim.x, p.nvec, skip);
 #pragma unroll
       for (int k = 0; k < B; ++k) {
         const int v = threadIdx.x + (k0 + k) * blockDim.x;
-        y[k0 + k] = silu_mul_vec<IO>(g[k], u[k]);
         if (v < p.nvec) {
           if (p.out_y) st_stream(p.out_y + row * p.nvec + v, y[k0 + k]);
           am = fmaxf(am, vec_absmax<IO>(y[k0 + k]));

@@ -83,6 +83,54 @@ def gpu_view(t):
     return t.view(torch.uint8)
 
 
+@pytest.mark.parametrize("M,H,mode", [(1201, 2176, "mxfp4"), (1201, 2176, "fp8_per_group128"),
+                                      (76001, 32, "mxfp4"), (25500, 96, "mxfp4"),
+                                      (19001, 128, "fp8_per_group128")])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+def test_two_vectors_a_thread(fx, M, H, mode, dtype):
+    """The group modes' form for many rows: aligned rows, rows on 16-byte boundaries
+    only, a row count, codes on a boundary that one store of 16 does not allow."""
+    x = rows(M, H, dtype, M + H)
+    r = fx.silu_mul_quant(x, mode, emit_y=True)
+    assert fx.mx_last_launch()[2] == 2
+    check_y(x, r.y)
+    check_codes(x, mode, r.q, r.scale, r.y)
+    wide = torch.zeros((M, 2 * H + 8), dtype=dtype, device="cuda")
+    wide[:, 8:] = x
+    s = fx.silu_mul_quant(wide[:, 8:], mode, emit_y=True)
+    assert fx.mx_last_launch()[2] == 2
+    for a, b in zip(r, s):
+        assert torch.equal(gpu_view(a), gpu_view(b))
+    q, used = torch.full_like(gpu_view(r.q), 0xA5), M - 3
+    count = torch.tensor([used], dtype=torch.int32, device="cuda")
+    fx.silu_mul_quant(x, mode, num_rows=count, out_q=q.view(r.q.dtype),
+                      out_scale=torch.empty_like(r.scale))
+    assert torch.equal(q[:used], gpu_view(r.q)[:used]) and (q[used:] == 0xA5).all()
+    step = 4 if mode == "mxfp4" else 8
+    flat = torch.empty(r.q.numel() + step, dtype=torch.uint8, device="cuda")
+    shifted = flat[step:].view(r.q.dtype).view(r.q.shape)
+    t = fx.silu_mul_quant(x, mode, out_q=shifted)
+    assert fx.mx_last_launch()[2] == 1
+    assert torch.equal(gpu_view(t.q), gpu_view(r.q))
+    assert torch.equal(gpu_view(t.scale), gpu_view(r.scale))
+
+
+@pytest.mark.parametrize("M,H,threads,vecs", [(601, 8, 32, 1), (601, 264, 64, 1), (601, 504, 32, 2),
+                                              (601, 520, 96, 1), (601, 1024, 32, 4),
+                                              (601, 2048, 64, 4), (601, 2560, 160, 2),
+                                              (601, 4104, 288, 2), (601, 16384, 512, 4),
+                                              (593, 32768, 512, 8), (3, 4096, 512, 1),
+                                              (3, 4104, 288, 2), (3, 32760, 512, 8)])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+def test_row_blocks(fx, M, H, threads, vecs, dtype):
+    """The per-token mode's blocks: few and many rows, idle lanes in the last vectors."""
+    x = rows(M, H, dtype, M + H)
+    r = fx.silu_mul_quant(x, "fp8_per_token", emit_y=True)
+    assert fx.mx_last_launch()[1:3] == (threads, vecs)
+    check_y(x, r.y)
+    check_codes(x, "fp8_per_token", r.q, r.scale, r.y)
+
+
 @pytest.mark.parametrize("H", [8, 24, 32, 40, 96])
 def test_short_rows(fx, H):
     for mode in ("fp8_per_token", "mxfp4"):
