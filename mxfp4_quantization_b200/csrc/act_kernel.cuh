@@ -149,8 +149,8 @@ struct SiluVecs {
 };
 
 // Recomputes the elements of `mask` (8 bits a vector) of N vectors, their gates at src
-// and every `step` vectors on, their ups nvec vectors behind (read again, 2 bytes each,
-// from L2): every lane its own next one, so lanes that missed different elements share
+// and every `step` vectors on, their ups nvec vectors behind (read again, 2 bytes
+// each, from L1): every lane its own next one, so lanes that missed different elements share
 // a pass.
 template <class IO, int N>
 __device__ __noinline__ SiluVecs<N> silu_mul_redo(SiluVecs<N> s, const uint4* src, int step,
@@ -242,16 +242,17 @@ __device__ __forceinline__ int64_t act_rows(const ActParams& p) {
 
 // Group modes (MXFP4, FP8 per 128): the rows laid end to end, N neighbouring 8-element
 // vectors a thread (two where there is work for it, one for decode-sized calls);
-// groups are 4 / N or 16 / N neighbouring lanes.  Bound by instructions: two
-// special-function operations an element, ten packed fp32 a pair, the interval
-// test, the quantization.  32768 x 2048: MXFP4 from bf16 63 us (4.8 TB/s), FP8 per 128
-// 71 us; from binary16, whose midpoints lie eight times as close, 77 and 84 us.
-// With vectors 256 apart instead of neighbours (their own scales and twice the
-// shuffles) and each one's open elements on their own 73, 85, 94 and 106 us; with
-// divisions for the rows 78, 89, 99 and 110.  A thread's 32 bytes in one load take the
-// same time.
+// groups are 4 / N or 16 / N neighbouring lanes.  Bound by instructions (24 an element:
+// two special-function operations, five packed fp32, the interval test, the
+// quantization; 70 % of the issue slots) and the loads' latency in front of them.
+// 32768 x 2048: MXFP4 from bf16 60 us (5.1 TB/s), FP8 per 128 67 us; from
+// binary16, whose midpoints lie eight times as close, 76 and 83 us.  Loads past L1
+// 60, 68, 76 and 84 us, with a thread's 32 bytes in one load (aligned rows only) the
+// same; five blocks an SM 62, 70, 76 and 83; vectors 256 apart instead of neighbours
+// (their own scales, twice the shuffles), each one's open elements on their own 73,
+// 85, 94 and 106.
 template <int MODE, class IO, int N>
-__global__ void __launch_bounds__(256, IO::kF16 ? 6 : 5) act_groups_kernel(const ActParams p) {
+__global__ void __launch_bounds__(256, 6) act_groups_kernel(const ActParams p) {
   pdl_enter();
   constexpr int kLanes = (MODE == MODE_MX ? 4 : 16) / N;
   const int lane = threadIdx.x & 31;
@@ -268,10 +269,11 @@ __global__ void __launch_bounds__(256, IO::kF16 ? 6 : 5) act_groups_kernel(const
   if (!ok) row = 0, v = 0;
   uint4 g[N], u[N], y[N];
   const uint4* src = p.x + row * p.ldv + v;
+  // (through L1: each of a thread's loads takes half of every 32-byte sector)
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    g[k] = ld_stream_nc(src + k);
-    u[k] = ld_stream_nc(src + p.nvec + k);
+    g[k] = __ldg(src + k);
+    u[k] = __ldg(src + p.nvec + k);
   }
   silu_mul_vecs<IO, N>(g, u, y, src, 1, p.nvec);
 #pragma unroll
@@ -319,9 +321,10 @@ __global__ void __launch_bounds__(256, IO::kF16 ? 6 : 5) act_groups_kernel(const
 }
 
 // Per-token mode: a block per row, the row in registers (V vectors a thread)
-// between the maximum and the codes.  bf16, 67 M elements: 65 us at H = 1024 and 2048
-// (5.2 TB/s), 68 us at 8192, 75 us at 16384, 103 us at 32768; the sizes of the blocks,
-// both ways, are at the launch.
+// between the maximum and the codes.  bf16, 67 M elements: 64 us at H = 1024 and 2048
+// (5.2 TB/s), 67 us at 8192, 74 us at 16384, 99 us at 32768; the sizes of the blocks,
+// both ways, are at the launch.  Three blocks of 512 threads an SM where four
+// vectors take two: 77 us at 2048 (spills).
 template <int V, class IO>
 __global__ void __launch_bounds__(512, V == 1 ? 4 : V == 2 ? 3 : V == 4 ? 2 : 1)
     act_row_kernel(const ActParams p) {
@@ -342,8 +345,8 @@ __global__ void __launch_bounds__(512, V == 1 ? 4 : V == 2 ? 3 : V == 4 ? 2 : 1)
         const int v = threadIdx.x + (k0 + k) * blockDim.x;
         const uint4* src = p.x + row * p.ldv + (v < p.nvec ? v : 0);
         if (v >= p.nvec) skip |= 0xFFu << (8 * k);
-        g[k] = ld_stream_nc(src);
-        u[k] = ld_stream_nc(src + p.nvec);
+        g[k] = __ldg(src);
+        u[k] = __ldg(src + p.nvec);
       }
       silu_mul_vecs<IO, B>(g, u, y + k0, p.x + row * p.ldv + threadIdx.x + k0 * blockDim.x,
                            blockDim.x, p.nvec, skip);

@@ -560,7 +560,7 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
   }
   // two vectors a thread once every SM has eight blocks of one, and where a thread's 16
   // codes are aligned to one store
-  // (MXFP4, 32768 x 2048: 63 us, with one vector 84 us)
+  // (MXFP4, 32768 x 2048: 60 us, with one vector 84 us)
   const int vecs =
       M * p.nvec > (int64_t)sms * 8 * 256 && aligned(out_q, mi.q == FN_MXFP4 ? 8 : 16) ? 2 : 1;
   const int units = p.nvec / vecs;
