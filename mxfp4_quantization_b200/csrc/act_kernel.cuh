@@ -107,16 +107,29 @@ __device__ __forceinline__ uint32_t silu_mul_mid(float g, float u) {
 }
 
 // The lower end of an interval that holds g u / (1 + e^-g); its product with
-// kSiluWidth is the upper one (g >= -87, |result| >= 2^-100).  e^-g = 2^t with t = -g log2(e) in two parts:
-// the rounded product and its remainder, which scales the result by 1 + t_lo ln 2.
+// kSiluWidth is the upper one (g >= -87, |g r| >= 2^-126, |result| >= 2^-100).  e^-g = 2^t
+// with t = -g log2(e) in two parts: the rounded product and its remainder, which scales
+// the result by 1 + t_lo ln 2.
 // Errors, in units of 2^-24: ex2.approx 4 (2^-22), the remainder's terms 1, their
 // product 1, the sum 1 + e^-g 1 (and it passes on at most the 6 before), the
 // approximate reciprocal 2, two products 2: below 12 in all.  The sum comes scaled by
 // 1 + 14 units, so the result is 2 to 26 below the real value, and 28 more, less
 // the rounding of that product, are above it.  (The .ftz forms: an e^-g below 2^-126 adds nothing to 1, and 1 + e^-g stays below 2^126,
-// so neither result that matters is subnormal.)
+// so neither result that matters is subnormal.  The product g r is a .ftz form too: a
+// bf16 gate below 2^-125 makes it subnormal, whose spacing swallows the 14 units, and a
+// large u would bring such a result back to any size; flushed, it stays 0 and counts
+// as outside the range.  It takes no time; a second minimum over the gates took 62 us
+// instead of 60, 32768 x 2048, MXFP4.)
 constexpr float kSiluUp = 1.f + 14 * 0x1p-24f;
 constexpr float kSiluWidth = 1.f + 28 * 0x1p-24f;
+
+__device__ __forceinline__ float2 mul_ftz_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.ftz.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -133,7 +146,7 @@ __device__ __forceinline__ float2 silu_mul_fp32(float2 g, float2 u) {
   const float2 d = fma_f32x2(e, make_float2(kSiluUp, kSiluUp), make_float2(kSiluUp, kSiluUp));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-  return mul_f32x2(mul_f32x2(g, r), u);  // g u alone can overflow where the result does not
+  return mul_f32x2(mul_ftz_f32x2(g, r), u);  // g u alone can overflow where the result does not
 }
 
 // The smallest value, NaN if one is.
@@ -206,9 +219,14 @@ __device__ __forceinline__ uint32_t silu_mul_fast(const uint4& gv, const uint4& 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float g0 = IO::lo(word(gv, i)), g1 = IO::hi(word(gv, i));
-        // outside the interval's range (a zero is exact, or far below every 16-bit value)
-        if (!(g0 >= -87.f) || !(fabsf(v[i].x) >= 0x1p-100f || v[i].x == 0.f)) mask |= 1u << (2 * i);
-        if (!(g1 >= -87.f) || !(fabsf(v[i].y) >= 0x1p-100f || v[i].y == 0.f)) mask |= 2u << (2 * i);
+        // outside the interval's range (a zero is exact, or far below every 16-bit value,
+        // if g r was not flushed)
+        const bool in0 = fabsf(v[i].x) >= 0x1p-100f ||
+                         (v[i].x == 0.f && (g0 == 0.f || fabsf(g0) >= 0x1p-100f));
+        const bool in1 = fabsf(v[i].y) >= 0x1p-100f ||
+                         (v[i].y == 0.f && (g1 == 0.f || fabsf(g1) >= 0x1p-100f));
+        if (!(g0 >= -87.f) || !in0) mask |= 1u << (2 * i);
+        if (!(g1 >= -87.f) || !in1) mask |= 2u << (2 * i);
       }
     }
   }
