@@ -117,6 +117,14 @@ __device__ __forceinline__ void mg_store_one(const MGParams& p, float a, int64_t
         (uint16_t)(p.out_type == MG_OUT_BF16 ? pack_bf16x2(a, 0.f) : pack_f16x2(a, 0.f));
 }
 
+// Whether out holds NaN there.
+__device__ __forceinline__ bool mg_is_nan(const MGParams& p, int64_t row, int f) {
+  if (p.out_type == MG_OUT_FP32)
+    return (reinterpret_cast<const uint32_t*>(p.out)[row * p.ldo + f] & 0x7fffffffu) > 0x7f800000u;
+  return (static_cast<const uint16_t*>(p.out)[row * p.ldo + f] & 0x7fffu) >
+         (p.out_type == MG_OUT_BF16 ? 0x7f80u : 0x7c00u);
+}
+
 // Stores `n` rows (of at most C) of a chunk; the lane holds feature f.
 template <int C>
 __device__ __forceinline__ void mg_store(const MGParams& p, uint32_t (&v)[C], int64_t row, int n,

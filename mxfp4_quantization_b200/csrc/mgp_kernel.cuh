@@ -30,6 +30,7 @@
 //
 //   warp 0       TMA
 //   warp 1       one thread of the first block: scale copies and MMAs
+//   warp 2       looks for rows without a source
 //   warps 4-11   epilogue, two per TMEM lane quadrant
 #pragma once
 #include "mg_common.cuh"
@@ -109,18 +110,6 @@ struct MGPTiles {
   }
 };
 
-// Zeros for a warp's feature f in the rows of a tile whose source index is outside the
-// operand (chunks of 32 rows from `first` on, every other one).
-__device__ __noinline__ void mgp_zero_outside(const MGParams& p, int row0, int n, int first, int f,
-                                              int lane) {
-  for (int c = first; c < n; c += 64) {
-    const int r = c + lane < n ? p.rows[row0 + c + lane] : 0;
-    uint32_t out = __ballot_sync(0xffffffffu, (unsigned)r >= (unsigned)p.x_rows);
-    for (; out && f < p.N; out &= out - 1)
-      mg_store_one(p, 0.f, (int64_t)row0 + c + __ffs(out) - 1, f);
-  }
-}
-
 __global__ void __launch_bounds__(kMgPairThreads, 1)
     mgp_kernel(const __grid_constant__ MGParams p, const __grid_constant__ MGMaps maps) {
   using S = MGPShape;
@@ -128,6 +117,7 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
   __shared__ __align__(8) uint64_t bars[2 * S::kStages + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t stop;
+  __shared__ uint32_t outside;  // a tile of this block has rows whose index is outside the operand
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -143,6 +133,7 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
 
   if (threadIdx.x == 0) {
     stop = 0;
+    outside = 0;
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
@@ -267,20 +258,18 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
         }
       }
     }
+  } else if (warp == 2) {
+    // ---- rows without a source ------------------------------------------------------------
+    bool out = false;
+    while (p.rows && tiles.next(t))
+      for (int r = lane; r < t.n; r += 32) out |= (unsigned)p.rows[t.row0 + r] >= (unsigned)p.x_rows;
+    if (out) outside = 1;
   } else if (warp >= 4) {
     // ---- epilogue ---------------------------------------------------------------------------
     const int quad = warp & 3;  // the TMEM lanes a warp can read
     bool ok = true;
     for (int i = 0; tiles.next(t); ++i) {
       const int acc = i & 1;
-      // the tile's source rows, on their way while its MMAs run
-      constexpr int kSrc = (kMgPairRows + 31) / 32;
-      int src[kSrc];
-      if (p.rows) {
-#pragma unroll
-        for (int j = 0; j < kSrc; ++j)
-          src[j] = j * 32 + lane < t.n ? p.rows[t.row0 + j * 32 + lane] : 0;
-      }
       if (ok) ok = mbar_wait<2>(tfull + 8 * acc, (i >> 1) & 1, &stop);
       tc_fence_after();
       const int f = t.f0 + (int)rank * kMgFeat + quad * 32 + lane;
@@ -298,17 +287,6 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_map(tempty + 8 * acc, 0));
-      // A row whose source index is outside the operand is zero: its codes are, but a
-      // weight's NaN scale made it NaN.  Over the stored row, so that tiles without such
-      // rows pay for these loads alone (a mask for every chunk: 32768 x 4096 x 7168
-      // 418 us instead of 403, 4096 x 4096 x 2048 49 instead of 45).
-      if (p.rows && ok) {
-        bool outside = false;
-#pragma unroll
-        for (int j = 0; j < kSrc; ++j) outside |= (unsigned)src[j] >= (unsigned)p.x_rows;
-        if (__any_sync(0xffffffffu, outside))  // (the lanes have met since their stores)
-          mgp_zero_outside(p, t.row0, t.n, (warp - 4) / 4 * 32, f, lane);
-      }
     }
   }
   __syncwarp();
@@ -316,6 +294,47 @@ __global__ void __launch_bounds__(kMgPairThreads, 1)
   __syncthreads();
   cluster_sync_all();
   if (warp == 1) tmem_dealloc<2>(tmem, S::kCols);
+  // A row without a source is zero.  Its codes are, so its sums are zero or, for a feature
+  // whose weight has a NaN scale, NaN, in all such rows of a tile alike: where the first
+  // one shows NaN, zeros are stored over all of them.  At the end, a warp a tile, so that
+  // the epilogue's loop stays as it is: 4096 gathered rows, 4096 x 2048, 46 us, 48 where a
+  // quarter of the rows has no source (50 and 52 with masks in that loop; 45 and 80 with
+  // zeros stored over every such row behind its tile).
+  if (outside) {
+    constexpr int kWarps = kMgPairThreads / 32, kParts = (kMgPairRows + 31) / 32;
+    MGPTiles own(p, table);  // every kWarps-th tile of the block
+    own.t += warp * own.stride;
+    own.stride *= kWarps;
+    while (own.next(t)) {
+      uint32_t out[kParts];
+      int first = -1;
+#pragma unroll
+      for (int j = 0; j < kParts; ++j) {
+        const int r = j * 32 + lane;
+        const int src = r < t.n ? p.rows[t.row0 + r] : 0;
+        out[j] = __ballot_sync(0xffffffffu, (unsigned)src >= (unsigned)p.x_rows);
+      }
+#pragma unroll
+      for (int j = kParts - 1; j >= 0; --j)
+        if (out[j]) first = j * 32 + __ffs(out[j]) - 1;
+      if (first < 0) continue;
+      const int f0 = t.f0 + (int)rank * kMgFeat + lane;
+      bool nan = false;
+#pragma unroll
+      for (int f = 0; f < kMgFeat; f += 32)
+        if (f0 + f < p.N) nan |= mg_is_nan(p, (int64_t)t.row0 + first, f0 + f);
+      if (!__any_sync(0xffffffffu, nan)) continue;
+#pragma unroll
+      for (int j = 0; j < kParts; ++j) {
+        for (; out[j]; out[j] &= out[j] - 1) {
+          const int64_t row = (int64_t)t.row0 + j * 32 + __ffs(out[j]) - 1;
+#pragma unroll
+          for (int f = 0; f < kMgFeat; f += 32)
+            if (f0 + f < p.N) mg_store_one(p, 0.f, row, f0 + f);
+        }
+      }
+    }
+  }
 }
 
 // Brings row-major (or row-tiled) scales into 512-byte tiles aligned to the pair

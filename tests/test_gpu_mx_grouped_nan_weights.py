@@ -48,3 +48,29 @@ def test_outside_rows_are_zero(fx, counts, dtype, tiled):  # noqa: F811
         exact, mass = mx_ref.product(a[src[inside]], mx_ref.values(bq[e], bs[e]))
         mx_ref.check_product(got[inside], exact, mass, K)
         assert bool((got[~inside] == 0).all()), (e, int((got[~inside] != 0).sum()))
+
+
+def test_many_tiles_a_pair(fx):  # noqa: F811
+    """More tiles of a pair of blocks than it has warps; an expert without NaN between
+    two with it, rows outside in some experts alone."""
+    E, n, N, K, a_rows = 100, 40, 4096, 64, 50
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * n
+    aq, as_ = mx_ref.codes(a_rows, K, 1), mx_ref.scales(a_rows, K, 1)
+    bq, bs = mx_ref.codes(E * N, K, 2).view(E, N, -1), mx_ref.scales(E * N, K, 2).view(E, N, -1)
+    bs[::2, ::129, 1] = 255
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rows = torch.randint(0, a_rows, (E, n), generator=g, device="cuda", dtype=torch.int32)
+    rows[::3, 5::7] = a_rows
+    out = torch.full((E * n, N), 7.0, dtype=BF, device="cuda")
+    fx.grouped_gemm(aq, as_, bq, bs, off, rows=rows.flatten(), out=out)
+    kind, (blocks, _, tok, _) = fx.mx_last_variant(), fx.mx_last_launch()
+    assert kind == fx.MX_VARIANT_GEMM_PAIR and E * N // 256 * -(-n // tok) > 12 * blocks // 2
+    a = mx_ref.values(aq, as_)
+    for e in range(E):
+        src = rows[e].long()
+        inside = src < a_rows
+        got = out[e * n:e * n + n]
+        exact, mass = mx_ref.product(a[src[inside]], mx_ref.values(bq[e], bs[e]))
+        mx_ref.check_product(got[inside], exact, mass, K)
+        assert bool((got[~inside] == 0).all()), e
