@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kMgThreads, 2)
         }
         if (p.rows) {
           __syncwarp();
-          if (lane < pieces) tma_gather4<1>(x_tile(s) + lane * 512, &maps.x, kb * 128, src, bar);
+          if (lane < pieces) tma_gather4(x_tile(s) + lane * 512, &maps.x, kb * 128, src, bar);
         }
         ++issued;
         if (++s == S::kStages) s = 0, ph ^= 1;

@@ -19,7 +19,6 @@ enum : int {
 constexpr int kMgFeat = 128;         // output features of a block's tile
 constexpr int kMgStageK = 256;       // elements of a K step (128 bytes of codes a row)
 constexpr int kMgThreads = 256;      // 4 role warps, 4 epilogue warps
-constexpr int kMgMaxExperts = 1024;  // the tile table in shared memory
 
 struct MGParams {
   const uint8_t* x_scale;   // token rows' scales
