@@ -58,9 +58,9 @@ SUBNORMAL = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float
 
 def product_tolerance(exact, mass, K, dtype):
     """Per element: the sums run in fp32 over steps of 64 elements.  One step adds
-    its 64 exact products to the running sum: the aligned addition of 65 terms
-    loses at most one unit of the last place (2^-23) of the largest of them per
-    term, and no term or running sum exceeds `mass`.  Then one rounding to the
+    its 64 exact products and the running sum on a common exponent, wide enough
+    that only the cut of the result to 24 bits counts: less than one unit of its
+    last place, 2^-23 of a sum that does not exceed `mass`.  Then one rounding to the
     output type, half a step."""
     fp32 = (K + 63) // 64 * 2.0 ** -23 * mass
     return fp32 + HALF_STEP[dtype] * (exact.abs() + fp32) + SUBNORMAL[dtype]
