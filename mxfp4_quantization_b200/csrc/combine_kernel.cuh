@@ -18,9 +18,9 @@ struct CombineParams {
 
 // Bound by memory: k rows read, one written.  B choices' rows are in flight together;
 // four, or two where there are no more (more registers then only cost blocks
-// an SM).  4096 tokens x 8 rows of 7168: 76 us (6.9 TB/s, part of it from L2)
-// with four, 77 with two, 85 with eight or with each load behind its position;
-// 1024 x 2 of 8192: 8.6 us with two, 10.5 with four.
+// an SM).  4096 tokens x 8 rows of 7168: 78 us (6.7 TB/s, part of it from L2)
+// with four, 80 with two, 85 with eight or with each load behind its position;
+// 1024 x 2 of 8192: 8.5 us with two, 10.3 with four.
 template <class IO, int kCombineBatch>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
   pdl_enter();
@@ -63,7 +63,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
                        IO::pack(a[2].x, a[2].y), IO::pack(a[3].x, a[3].y)));
 }
 
-// Rows that are not made of aligned 16-byte vectors: a thread per element.
+// Rows that are not made of aligned 16-byte vectors: a thread per element, each
+// choice's load behind its position's.  Bound by that latency and by instructions: 4096
+// tokens x 8 rows of 7167 take 303 us (1.7 TB/s), 4 x 8 of them 2.3 us.
 template <class IO>
 __global__ void __launch_bounds__(256) combine_narrow_kernel(const CombineParams p) {
   pdl_enter();

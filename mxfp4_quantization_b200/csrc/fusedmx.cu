@@ -236,7 +236,7 @@ struct Plan {
   int64_t workspace() const { return x_bytes + w_bytes + code_bytes; }
 };
 
-constexpr int kSms = 148;  // B200
+constexpr int kSms = 148;  // B200 (a constant, so that a plan follows from the sizes alone)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -248,9 +248,12 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
   const int64_t more = grouped ? std::min(E, M) : 0;  // a partly filled tile an expert
   const int64_t groups = K / 32, kts = ceil_div(groups, 4);
   // Pairs of blocks from here on.  Measured, us a call of single blocks / of pairs,
-  // 8192 x 7168: 64 rows 14.2 / 15.2, 96 rows 16.3 / 15.6, 128 rows 18.4 / 15.7;
-  // experts of 4096 x 7168 with 32 rows on average 256 / 177 (64 experts), 39 / 34
-  // (8 experts); 2048 x 2048 with 50 rows 12.0 / 13.0 (4 experts).
+  // 8192 x 7168: 64 rows 13.1 / 14.0, 96 rows 15.4 / 14.5, 128 rows 15.6 / 14.6;
+  // experts of 4096 x 7168 with 16 rows on average 157 / 162 (64 experts), 25 / 29 (8
+  // experts), with 32 rows 157-167 / 165-170 and 27 / 30, with 48 rows 168 / 167;
+  // 2048 x 2048 with 50 rows 10.1 / 9.4 (4 experts).  (Between 17 and 48 rows single
+  // blocks are up to a tenth ahead; the border of 16, above which a call takes a
+  // workspace, is part of the header's contract and dates from an earlier form of them.)
   p.pair = each > (grouped ? MX_SMALL_EXPERT_ROWS : MX_SMALL_ROWS);
   if (p.pair) {
     p.feat = ceil_div(N, fn::kMgPairFeat);
@@ -274,8 +277,9 @@ int plan_product(int64_t M, int64_t E, int64_t N, int64_t K, int flags, bool gro
     p.tok = each <= 16 ? 16 : 64;
     p.pieces = M / p.tok + (grouped ? more : M % p.tok != 0);
     // few tiles: the blocks of a cluster share the K steps of one, while all of them
-    // fit the GPU at once, two an SM.  16 x 8192 x 7168: 11.7 us in two, 11.2 in four,
-    // 16.2 in eight parts (512 blocks); 1 x 7168 x 7168: 10.5, 9.5, 14.2.
+    // fit the GPU at once, two an SM.  16 x 8192 x 7168: 14.1 us whole, 11.4 in two,
+    // 10.8 in four, 15.8 in eight parts (512 blocks); 1 x 7168 x 7168: 14.0, 10.4, 9.7,
+    // 14.5.
     const int64_t steps = ceil_div(K, fn::kMgStageK), tiles = p.feat * p.pieces;
     while (p.split < 8 && tiles * p.split * 2 <= 2 * kSms && p.split * 4 <= steps) p.split *= 2;
   }
@@ -312,7 +316,7 @@ int launch_product(const Product& q, bool grouped, const Plan& plan, void* strea
   p.out_quads = p.out_type != MX_OUT_FP32 && q.N % 4 == 0 && q.ldo % 4 == 0 && aligned(q.out, 8);
   // fp32 rows in 8-byte stores where the epilogue sets the pace, in 4-byte stores where
   // the MMAs do and its shuffles cost them issue slots: 8192 x 7168, K = 2048
-  // 80 us / 90 us, 8192 x 8192, K = 7168 184 us / 180 us
+  // 78 us / 86 us, 8192 x 8192, K = 7168 221 us / 201 us
   p.out_pairs = p.out_type == MX_OUT_FP32 && q.K <= 4096 && q.N % 2 == 0 && q.ldo % 2 == 0 &&
                 aligned(q.out, 8);
   p.tok = plan.tok;
@@ -543,8 +547,8 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
     // Few rows: one vector a thread up to 512 threads.  Many: up to four, in blocks as
     // small as a warp (the barriers of a row then hold up few warps), unless more
     // than an eighth of the lanes would idle.  32768 x 2048: 65 us with four
-    // (64 threads), 69 with two, 87 with one; 4097 x 2560: 14.3 with four (96 threads,
-    // a sixth idle), 13.6 with two.
+    // (64 threads), 70 with two, 89 with one; 4097 x 2560: 14.5 with four (96 threads,
+    // a sixth idle), 13.4 with two.
     const auto threads_of = [&](int v) { return round_up(ceil_div(p.nvec, v), 32); };
     int V = 1;
     while (M > (int64_t)sms * 4 && V < 4 && p.nvec > 32 * V &&
@@ -560,7 +564,7 @@ int mx_silu_mul_quant(const void* x, int64_t ldx, int mode, int64_t M, int64_t H
   }
   // two vectors a thread once every SM has eight blocks of one, and where a thread's 16
   // codes are aligned to one store
-  // (MXFP4, 32768 x 2048: 60 us, with one vector 84 us)
+  // (MXFP4, 32768 x 2048: 60 us, with one vector 80 us)
   const int vecs =
       M * p.nvec > (int64_t)sms * 8 * 256 && aligned(out_q, mi.q == FN_MXFP4 ? 8 : 16) ? 2 : 1;
   const int units = p.nvec / vecs;

@@ -9,23 +9,28 @@
 //
 // TMEM: two accumulators of 240 columns and one K step's scales (24 columns).
 // 256-row tiles leave room for two accumulators only if they overlap, and the
-// next tile's first MMA then waits for the epilogue: 1.6 us a tile, measured.
+// next tile's first MMA then waits for the epilogue: 1.6 us a tile (*).
 //
 // All operands come by TMA.  Scales have to be 512-byte tiles aligned to the row
 // tiles, which start anywhere (an expert's first row, a multiple of the tile
 // height): mgp_arrange_kernel writes them to the workspace first, with zeros in
 // the padding, and gathers the codes of rows given by index once instead of once
 // per feature tile (with gather4 in the product itself, 32768 rows x 4096 features
-// took 1140 us against 800 us without an index).  Warps that fetched the
-// row-major scales inside the product cost 60 us of 320 (8192 x 8192 x 7168):
-// their tiles pass a fence and a release to the other block in every K step.
+// took 1140 us against 800 us without an index (*); 32 experts' 32768 gathered rows
+// take 407 us, the same rows in place 390).
+// Warps that fetched the row-major scales inside the product cost 60 us of 320
+// (8192 x 8192 x 7168 (*)): their tiles pass a fence and a release to the other block
+// in every K step.
+//
+// (*) Measured while the MMAs were still issued from a one-lane branch, which set the
+// pace (251 us instead of 170); not measured again on this form.
 //
 // What bounds it: 8192 x 8192 x 7168 takes 166-182 us (5300-5800 TFLOP/s; the arranging
 // kernel's 6 us in front included), tensor pipe 77 % busy, L2 to shared memory 13 TB/s,
 // at the power limit when calls follow each other (215 us).  The scale copies, in
 // order with the MMAs, cost the rest of a K step.  Measured and not kept: copies a K
-// step ahead into a second buffer; scales stored four times and copied 128 rows at
-// a time (same time); warps that store the words to TMEM (tcgen05.st: 474 us);
+// step ahead into a second buffer (*); scales stored four times and copied 128 rows at
+// a time (same time); warps that store the words to TMEM (tcgen05.st: 474 us (*));
 // heights of 208 and 192 rows (184 us); rows' codes in one box instead of three.
 //
 //   warp 0       TMA
@@ -65,8 +70,8 @@ struct MGPTile {
 
 // The tiles in order: expert, group of eight row tiles, feature tile, row tile.  The
 // 74 pairs then work on about 9 x 8 tiles at a time, whose operands stay in L2
-// (with all row tiles in one group 32768 x 4096 x 7168 read its 117 MB of rows once
-// per feature tile: 523 us against 463).
+// (with all row tiles in one group 32768 x 4096 x 7168 reads its 117 MB of rows once
+// per feature tile: 405 us against 323).
 struct MGPTiles {
   static constexpr int kGroup = 8;
   const int* cum;  // [E + 1] row tiles before expert e   (offsets given)

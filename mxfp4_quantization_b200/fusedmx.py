@@ -11,6 +11,9 @@ Scales are told apart by their shape, as fusednorm.alloc_outputs makes them:
 [rows, K/32] is row-major, a flat buffer is the 32x4x4 tiling
 (FN_SCALE_SWIZZLE_32_4_4).
 
+The operators are for inference: outputs carry no gradient, whatever the inputs
+require.
+
 There is no fallback: if the library is missing, importing this module fails.
 """
 import ctypes
